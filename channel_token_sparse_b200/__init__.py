@@ -22,12 +22,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libds.so")
 
 DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED, DS_ERR_CUDA, DS_ERR_WORKSPACE, DS_ERR_TIMEOUT = range(6)
-DS_F32, DS_BF16, DS_F16, DS_INT4 = range(4)
+DS_F32, DS_BF16, DS_F16, DS_INT4, DS_E4M3 = range(5)
+DS_ROPE_HALF, DS_ROPE_INTERLEAVED = range(2)
 DS_FALLBACK_PER_ENTRY, DS_FALLBACK_BATCH = range(2)
 DS_CRIT_LEANK_RATIO, DS_CRIT_Q_OUTLIER, DS_CRIT_K_OUTLIER, DS_CRIT_QK_OUTLIER, DS_CRIT_QK_CHUNKED = range(5)
 
 # every C-ABI entry point: name -> (restype, argtypes)
-_vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+_vp, _i, _f, _sz, _ll = C.c_void_p, C.c_int, C.c_float, C.c_size_t, C.c_longlong
 SIGNATURES = {
     "ds_status_string": (C.c_char_p, [_i]),
     "ds_last_error": (C.c_char_p, []),
@@ -57,6 +58,17 @@ SIGNATURES = {
     "ds_check_device": (_i, [_vp]),
     "ds_selftest_bounded_wait": (_i, [_i, _vp]),
     "ds_sparse_decode_workspace": (_i, [_i, _i, _i, _i, _i, _i, _i, C.POINTER(_sz)]),
+    "ds_write_kv": (_i, [_vp, _ll, _ll, _vp, _ll, _ll, _vp, _ll, _ll, _i, _vp, _vp, _f, _vp, _i, _i, _vp, _vp, _vp,
+                         _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp]),
+    "ds_write_kv_paged": (_i, [_vp, _ll, _ll, _vp, _ll, _ll, _vp, _ll, _ll, _i, _vp, _vp, _f, _vp, _i, _i, _vp, _vp,
+                               _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "ds_read_kv": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _i, _vp]),
+    "ds_read_kv_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i, _i, _i, _vp, _vp, _i, _i, _vp]),
+    "ds_tree_decode_workspace_size": (_i, [_i, _i, _i, _i, _i, _i, _i, C.POINTER(_sz)]),
+    "ds_tree_decode": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp,
+                            _sz, _vp]),
+    "ds_tree_decode_paged": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                  _f, _vp, _i, _vp, _sz, _vp]),
     "ds_dense_decode": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp]),
 }
 
@@ -504,3 +516,327 @@ def dense_decode(q, k, v, s: int, out=None, out_dtype=None, sm_scale: float = 0.
     _check(lib().ds_dense_decode(_ptr(q), _ptr_kv(k), _ptr_kv(v), _kv_dtype(k), b, hq, hkv, s, s_cap, d,
                                  float(sm_scale), _ptr(out), odt, _stream(stream)))
     return out
+
+
+# ------------------------------------------- writing and reading caches, trees
+
+def _cache_dtype(t) -> int:
+    return DS_E4M3 if t.dtype == _torch().float8_e4m3fn else _kv_dtype(t)
+
+
+def _int32(name, t, *shape):
+    """A contiguous int32 tensor of the given shape, or None."""
+    if t is not None and (t.dtype != _torch().int32 or tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be int32 of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _scales(dt, k, v, k_scale, v_scale):
+    if dt != DS_E4M3:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to 8-bit caches")
+        return
+    torch = _torch()
+    for c, sc in ((k, k_scale), (v, v_scale)):
+        if c is not None and (sc is None or sc.dtype != torch.float32 or sc.shape != c.shape[:-1]):
+            raise ValueError("an 8-bit cache needs a float32 scale of its shape without the last dimension")
+
+
+def _same_caches(k, v):
+    if v is not None and (k.dtype != v.dtype or k.shape != v.shape):
+        raise ValueError("the key and value caches must have one dtype and shape")
+    if k.dim() != 4:
+        raise ValueError("a cache has four dimensions")
+
+
+def _on_one_device(*ts):
+    """The device of all given CUDA tensors."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+class _Prepared:
+    """A C-ABI call with its arguments checked and converted once. Calling it
+    enqueues the call on `stream`, or on the stream that is current on the
+    tensors' device at that time, and returns the outputs."""
+
+    def _bind(self, fn, args, dev, stream, keep, result):
+        self._fn, self._args, self._dev, self._stream = fn, args, dev, stream
+        self._keep = keep  # keeps the memory alive
+        self._result = result
+
+    def __call__(self):
+        torch = _torch()
+        dev, stream = self._dev, self._stream
+        if torch.cuda.current_device() != dev.index:
+            with torch.cuda.device(dev):
+                s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+                st = self._fn(*self._args, s)
+        else:
+            s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+            st = self._fn(*self._args, s)
+        if st != DS_OK:
+            raise DSError(st, last_error())
+        return self._result
+
+
+def _alloc(shape, dtype, dev, stream):
+    """torch.empty in the memory pool of the stream that will use it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def new_kv_cache(shape, dtype, device="cuda"):
+    """Zeroed caches k, v of `shape` ([B, Hkv, S_cap, D], or a pool
+    [num_blocks, Hkv, page, D]) and, for torch.float8_e4m3fn, their scales:
+    (k, v, k_scale, v_scale)."""
+    torch = _torch()
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) if dtype == torch.float8_e4m3fn
+            else torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return k, v, None, None
+    return k, v, *(torch.zeros(tuple(shape)[:-1], dtype=torch.float32, device=device) for _ in range(2))
+
+
+class PreparedWriteKV(_Prepared):
+    """write_kv bound once; calling it enqueues the write and returns q_out."""
+
+    def __init__(self, q, k, v, k_cache, v_cache, starts=None, positions=None, lens=None, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, inv_freq=None, rope: int = DS_ROPE_HALF, k_scale=None,
+                 v_scale=None, block_table=None, q_out=None, stream=None):
+        torch = _torch()
+        dev = _on_one_device(k, v, q, k_cache, v_cache, starts, positions, lens, q_weight, k_weight, inv_freq,
+                             k_scale, v_scale, block_table, q_out)
+        for t in (k_cache, v_cache, starts, positions, lens, q_weight, k_weight, inv_freq, k_scale, v_scale,
+                  block_table, q_out):
+            if t is not None and not t.is_contiguous():
+                raise ValueError("all tensors but q, k and v must be contiguous")
+        for t in (k, v) if q is None else (k, v, q):
+            if t.dim() != 4 or t.dtype != k.dtype or t.shape[:2] != k.shape[:2] or t.shape[3] != k.shape[3]:
+                raise ValueError("q, k, v must be [B, T, heads, D] of one dtype")
+            if t.numel() and (t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != t.shape[3])):
+                raise ValueError("the heads of a token of q, k, v must be contiguous")
+        if k.shape != v.shape:
+            raise ValueError("k and v must have one shape")
+        dt, cdt = _kv_dtype(k), _cache_dtype(k_cache)
+        _same_caches(k_cache, v_cache)
+        _scales(cdt, k_cache, v_cache, k_scale, v_scale)
+        b, t, hkv, d = k.shape
+        if k_cache.shape[1] != hkv or k_cache.shape[3] != d:
+            raise ValueError("the caches' heads or head size differ from k's")
+        _int32("starts", starts, b)
+        _int32("lens", lens, b)
+        _int32("positions", positions, b, t)
+        for w in (q_weight, k_weight):
+            if w is not None and (w.dtype != k.dtype or tuple(w.shape) != (d,)):
+                raise ValueError("a norm weight must be [D] of q's dtype")
+        rot = 0
+        if inv_freq is not None:
+            if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+                raise ValueError("inv_freq must be a float32 vector")
+            rot = 2 * inv_freq.shape[0]
+        hq = 0
+        if q is not None:
+            hq = q.shape[2]
+            if q_out is None:
+                q_out = _alloc((b, t, hq, d), q.dtype, dev, stream)
+            elif tuple(q_out.shape) != (b, t, hq, d) or q_out.dtype != q.dtype:
+                raise ValueError("q_out must have q's shape and dtype")
+        elif q_out is not None or q_weight is not None:
+            raise ValueError("q_out and q_weight need q")
+
+        def strided(x):
+            return (None, 0, 0) if x is None else (x.data_ptr(), x.stride(0), x.stride(1))
+
+        def ptr(x):
+            return None if x is None else x.data_ptr()
+
+        args = [*strided(q), *strided(k), *strided(v), dt, ptr(q_weight), ptr(k_weight), float(eps), ptr(inv_freq), rot,
+                int(rope), ptr(positions), ptr(starts), ptr(lens), b, t, hq, hkv]
+        tail = [d, ptr(q_out), ptr(k_cache), ptr(v_cache), cdt, ptr(k_scale), ptr(v_scale)]
+        if block_table is None:
+            if k_cache.shape[0] != b:
+                raise ValueError("the caches' batch differs from k's")
+            fn, args = lib().ds_write_kv, args + [k_cache.shape[2]] + tail
+        else:
+            _int32("block_table", block_table, b, *block_table.shape[1:2])
+            fn = lib().ds_write_kv_paged
+            args = args + tail + [ptr(block_table), block_table.shape[1], k_cache.shape[2], k_cache.shape[0]]
+        self.q_out = q_out
+        self._bind(fn, args, dev, stream, (q, k, v, k_cache, v_cache, starts, positions, lens, q_weight, k_weight,
+                                           inv_freq, k_scale, v_scale, block_table), q_out)
+
+
+def write_kv(q, k, v, k_cache, v_cache, **kw):
+    """Write the keys and values of T new tokens an entry, k and v [B, T, Hkv,
+    D] as the projections left them, into the caches at rows starts[b] + i,
+    with the per-head norm (k_weight), the rotation (inv_freq, positions) and
+    the 8-bit quantisation (k_scale, v_scale) in the same pass; q [B, T, Hq, D]
+    (or None) gets its norm and rotation into q_out, which is returned. q, k
+    and v may be views of one fused projection. Caches [B, Hkv, S_cap, D], or
+    pools with block_table. Arguments as PreparedWriteKV's; see ds_write_kv."""
+    return PreparedWriteKV(q, k, v, k_cache, v_cache, **kw)()
+
+
+def read_kv(k, v, k_scale, v_scale, s: int, seq_lens=None, block_table=None, dtype=None, k_out=None, v_out=None,
+            stream=None):
+    """Rows [0, s) of an 8-bit cache (k, v torch.float8_e4m3fn, dense or pools
+    with block_table) as dtype (bf16 by default) rows: (k_out, v_out), each
+    [B, Hkv, s, D] unless given (then [B, Hkv, >= s, D]). v, v_scale None: the
+    keys alone. Rows past seq_lens[b] are not written."""
+    torch = _torch()
+    dev = _on_one_device(k, v, k_scale, v_scale, seq_lens, block_table, k_out, v_out)
+    for t in (k, v, k_scale, v_scale, seq_lens, block_table, k_out, v_out):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    if _cache_dtype(k) != DS_E4M3:
+        raise TypeError("read_kv reads float8_e4m3fn caches")
+    _same_caches(k, v)
+    _scales(DS_E4M3, k, v, k_scale, v_scale)
+    b = k.shape[0] if block_table is None else block_table.shape[0]
+    hkv, d = k.shape[1], k.shape[3]
+    _int32("seq_lens", seq_lens, b)
+    if k_out is None:
+        k_out = _alloc((b, hkv, s, d), dtype or torch.bfloat16, dev, stream)
+    if v is None:
+        if v_out is not None or v_scale is not None:
+            raise ValueError("v_out and v_scale need v")
+    elif v_out is None:
+        v_out = _alloc(k_out.shape, k_out.dtype, dev, stream)
+    for o in (k_out,) if v is None else (k_out, v_out):
+        if o.dim() != 4 or o.shape[0] != b or o.shape[1] != hkv or o.shape[3] != d or o.shape != k_out.shape:
+            raise ValueError("k_out and v_out must be [B, Hkv, S, D]")
+        if o.dtype != k_out.dtype or (dtype is not None and o.dtype != dtype):
+            raise ValueError("k_out and v_out must have one dtype")
+
+    def ptr(x):
+        return None if x is None else x.data_ptr()
+
+    tail = [ptr(k_out), ptr(v_out), _kv_dtype(k_out), k_out.shape[2]]
+    call = _Prepared()
+    if block_table is None:
+        fn, args = lib().ds_read_kv, [ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), ptr(seq_lens), b, hkv, int(s),
+                                      k.shape[2], d, *tail]
+    else:
+        _int32("block_table", block_table, b, *block_table.shape[1:2])
+        fn = lib().ds_read_kv_paged
+        args = [ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), ptr(block_table), block_table.shape[1], k.shape[2],
+                k.shape[0], ptr(seq_lens), b, hkv, int(s), d, *tail]
+    call._bind(fn, args, dev, stream, None, (k_out, v_out))
+    return call()
+
+
+def tree_mask(parents):
+    """The mask of drafted trees from their parents [B, T] (int tensor: the
+    index of each node's parent, which is a smaller one, or -1 for the prefix):
+    node i sees itself and its ancestors. int32 [B, T, ceil(T / 32)] on
+    parents' device; computed with torch, outside the decode path."""
+    torch = _torch()
+    b, t = parents.shape
+    p = parents.to("cpu", torch.int64)
+    if bool((p >= torch.arange(t)).any()) or bool((p < -1).any()):
+        raise ValueError("a parent must be -1 or an earlier node")
+    sees = torch.zeros((b, t, t), dtype=torch.bool)
+    for i in range(t):
+        has = (p[:, i] >= 0)[:, None]
+        sees[:, i] = sees[torch.arange(b), p[:, i].clamp_min(0)] & has
+        sees[:, i, i] = True
+    words = (t + 31) // 32
+    bits = torch.zeros((b, t, words * 32), dtype=torch.int64)
+    bits[:, :, :t] = sees.long()
+    bits = (bits.view(b, t, words, 32) << torch.arange(32)).sum(-1)
+    return torch.where(bits >= 1 << 31, bits - (1 << 32), bits).to(torch.int32).to(parents.device)
+
+
+def tree_decode_workspace(b, t, hq, hkv, s, d, kv_dtype=DS_BF16) -> int:
+    """Device scratch bytes tree_decode needs for a shape."""
+    out = C.c_size_t()
+    _check(lib().ds_tree_decode_workspace_size(b, t, hq, hkv, s, d, kv_dtype, C.byref(out)))
+    return out.value
+
+
+class PreparedTreeDecode(_Prepared):
+    """tree_decode bound once, with its output and workspace; calling it
+    enqueues the attention and returns out. set_length(s) moves to another
+    prefix length, up to the one it was made with."""
+
+    _S_ARG = {False: 13, True: 17}
+
+    def __init__(self, q, k, v, s: int, mask=None, seq_lens=None, node_lens=None, k_scale=None, v_scale=None,
+                 block_table=None, out=None, out_dtype=None, sm_scale: float = 0.0, ws=None, stream=None):
+        torch = _torch()
+        dev = _on_one_device(q, k, v, mask, seq_lens, node_lens, k_scale, v_scale, block_table, out, ws)
+        for t in (q, k, v, mask, seq_lens, node_lens, k_scale, v_scale, block_table, out, ws):
+            if t is not None and not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+        if q.dim() != 4:
+            raise ValueError("q must be [B, T, Hq, D]")
+        b, t, hq, d = q.shape
+        kdt = _cache_dtype(k)
+        _same_caches(k, v)
+        _scales(kdt, k, v, k_scale, v_scale)
+        if _kv_dtype(q) != (DS_F32 if kdt == DS_F32 else DS_BF16):
+            raise TypeError("q must be float32 with a float32 cache, else bfloat16")
+        if k.shape[3] != d:
+            raise ValueError("the caches' head size differs from q's")
+        hkv = k.shape[1]
+        _int32("mask", mask, b, t, (t + 31) // 32)
+        _int32("seq_lens", seq_lens, b)
+        _int32("node_lens", node_lens, b)
+        need = tree_decode_workspace(b, t, hq, hkv, s, d, kdt)
+        if out is None:
+            out = _alloc((b, t, hq, d), out_dtype or torch.float32, dev, stream)
+        elif out.shape != q.shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError("out must have q's shape (and out_dtype)")
+        if ws is None:
+            ws = _alloc((need,), torch.uint8, dev, stream)
+
+        def ptr(x):
+            return None if x is None else x.data_ptr()
+
+        head = [ptr(q), ptr(k), ptr(v), kdt, ptr(k_scale), ptr(v_scale), ptr(mask)]
+        tail = [d, float(sm_scale), ptr(out), _kv_dtype(out), ptr(ws), ws.numel() * ws.element_size()]
+        if block_table is None:
+            if k.shape[0] != b:
+                raise ValueError("the caches' batch differs from q's")
+            fn = lib().ds_tree_decode
+            args = head + [ptr(seq_lens), ptr(node_lens), b, t, hq, hkv, int(s), k.shape[2]] + tail
+        else:
+            _int32("block_table", block_table, b, *block_table.shape[1:2])
+            fn = lib().ds_tree_decode_paged
+            args = head + [ptr(block_table), block_table.shape[1], k.shape[2], k.shape[0], ptr(seq_lens),
+                           ptr(node_lens), b, t, hq, hkv, int(s)] + tail
+        self.out, self._s_at, self._s_max = out, self._S_ARG[block_table is not None], int(s)
+        self._bind(fn, args, dev, stream, (q, k, v, mask, seq_lens, node_lens, k_scale, v_scale, block_table, ws), out)
+
+    def set_length(self, s: int) -> None:
+        if not 0 <= s <= self._s_max:
+            raise ValueError(f"prefix length {s} outside [0, {self._s_max}]")
+        self._args[self._s_at] = int(s)
+
+
+def tree_decode(q, k, v, s: int, **kw):
+    """Attention of the T drafted tokens q [B, T, Hq, D] over caches k, v
+    [B, Hkv, S_cap, D] that hold a prefix of s tokens (seq_lens[b], at most s)
+    and, in the T rows behind it, the drafted tokens' own keys and values;
+    mask as tree_mask makes it (None: a chain). float8_e4m3fn caches need
+    k_scale and v_scale. Returns out [B, T, Hq, D]. Arguments as
+    PreparedTreeDecode's; see ds_tree_decode."""
+    return PreparedTreeDecode(q, k, v, s, **kw)()
+
+
+def tree_decode_paged(q, k_pool, v_pool, block_table, s: int, **kw):
+    """tree_decode over pools [num_blocks, Hkv, page, D] with block_table
+    [B, max_blocks]."""
+    return PreparedTreeDecode(q, k_pool, v_pool, s, block_table=block_table, **kw)()

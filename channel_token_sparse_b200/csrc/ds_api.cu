@@ -386,6 +386,20 @@ ds_status run_label(const void* k, ds_dtype kdt, const int32_t* idx, int b, int 
 
 }  // namespace
 
+namespace ds {
+
+int report(int status, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return status;
+}
+
+cudaError_t device_status_word(unsigned int** out) { return status_word(out); }
+
+}  // namespace ds
+
 extern "C" {
 
 const char* ds_status_string(ds_status st) {
@@ -444,7 +458,7 @@ ds_status ds_check_device(cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e, "clearing the device status");
     return fail(DS_ERR_TIMEOUT, "a kernel gave up a bounded wait (sites 0x%x: bit 0 self-test, "
-                "bit 1 label build stage, bit 2 decode stage)", w);
+                "bit 1 label build stage, bit 2 decode stage, bit 3 tree decode stage)", w);
 }
 
 ds_status ds_calibrate_workspace_size(int n_samples, int hq, int hkv, int w, int s, int d,

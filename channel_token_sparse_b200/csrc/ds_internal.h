@@ -25,6 +25,47 @@ DecodeKernel decode_kernel_bf16_i4_paged(int D, int C, int GT);
 // the key of the per-context caches of __device__ variable addresses.
 bool current_context_id(unsigned long long* id);
 
+// Records a failure's reason for ds_last_error and returns its status.
+int report(int status, const char* fmt, ...);
+// The library's device status word in the current context (bounded waits).
+cudaError_t device_status_word(unsigned int** out);
+
+// Cache rows of token t of (entry e, kv head h): dense [b, hkv, s_cap] when
+// block_table is NULL, else through the table into a pool [num_blocks, hkv, page].
+struct CacheRows {
+    const int32_t* block_table = nullptr;
+    int max_blocks = 0, page_shift = 0, num_blocks = 0;
+    int hkv = 0, s_cap = 0;
+};
+
+struct WriteArgs {
+    const void *q, *k, *v;
+    long long q_bs, q_ts, k_bs, k_ts, v_bs, v_ts;
+    const void *q_weight, *k_weight;
+    float eps;
+    const float* inv_freq;
+    int rot_dim, interleaved;
+    const int32_t *positions, *starts, *lens;
+    int b, t, hq, hkv, d, rows;  // rows: cache rows an entry can address
+    bool f32, e4m3;              // element type of q/k/v (f32 or bf16); cache in e4m3
+    void *q_out, *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    CacheRows at;
+};
+cudaError_t launch_write_kv(const WriteArgs& a, cudaStream_t st);
+
+struct ReadArgs {
+    const void *k, *v;
+    const float *k_scale, *v_scale;
+    const int32_t* seq_lens;
+    int b, hkv, s, d;
+    void *k_out, *v_out;
+    bool f32;
+    int s_out_cap;
+    CacheRows at;
+};
+cudaError_t launch_read_kv(const ReadArgs& a, cudaStream_t st);
+
 struct LabelArgs {
     const void* k;
     bool kdt_bf16;

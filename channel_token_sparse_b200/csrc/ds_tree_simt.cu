@@ -1,0 +1,216 @@
+// ds_tree_simt.cu -- tree attention with fp32 arithmetic on the CUDA cores.
+//
+// One pass over an item's tokens with the running maximum and sum of each
+// row's softmax: for a tile of 64 tokens the scores s = qscale * q.k (base-2
+// exponents) of 32 query rows, their new maxima, weights 2^(s - m), and the
+// weighted values, all in fp32. A tile's K and V rows are converted to fp32 in
+// shared memory once and serve the 32 rows.
+#include <math.h>
+
+#include "ds_tree.cuh"
+
+namespace ds {
+
+namespace {
+
+constexpr int kNT = 256;
+constexpr int kR = 32;     // query rows of a row tile
+constexpr int kT = 64;     // tokens of a token tile
+
+__device__ __forceinline__ float e4m3_lo(uint32_t w, int j) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * (j >> 1)))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return (j & 1) ? f.y : f.x;
+}
+
+// Four consecutive channels of cache row `row`, times its scale.
+template <int TYPE, int D>
+__device__ __forceinline__ float4 load4(const void* base, const float* scale, long long row, int c) {
+    if constexpr (TYPE == kTreeF32) {
+        const uint4 w = ldg_stream16(static_cast<const float*>(base) + row * D + c);
+        return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+    } else if constexpr (TYPE == kTreeBF16) {
+        const uint2 w = ldg_stream8(static_cast<const uint16_t*>(base) + row * D + c);
+        return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+    } else {
+        const uint32_t w = ldg_stream4(static_cast<const uint8_t*>(base) + row * D + c);
+        const float sc = __ldg(scale + row);
+        return make_float4(e4m3_lo(w, 0) * sc, e4m3_lo(w, 1) * sc, e4m3_lo(w, 2) * sc, e4m3_lo(w, 3) * sc);
+    }
+}
+
+template <int D> constexpr int simt_smem() { return (kR * D + kT * (D + 4) + kT * D + kR * (kT + 4) + 3 * kR) * 4; }
+
+template <int TYPE, int D>
+__global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const TreeParams p) {
+    extern __shared__ __align__(16) float sm[];
+    float* sq = sm;                     // [kR][D] queries, times qscale
+    float* sk = sq + kR * D;            // [kT][D + 4]
+    float* sv = sk + kT * (D + 4);      // [kT][D]
+    float* ss = sv + kT * D;            // [kR][kT + 4] scores, then weights
+    float* s_m = ss + kR * (kT + 4);    // [kR] running maximum
+    float* s_l = s_m + kR;              // [kR] running sum
+    float* s_w = s_l + kR;              // [kR] factor of what was summed so far
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int tid = threadIdx.x;
+    const long long total = tree_total(p);
+    long long u = share_begin(total, blockIdx.x, p.grid);
+    const long long end = share_begin(total, blockIdx.x + 1, p.grid);
+    if (u >= end) return;
+    TreeCursor cur = tree_seek(p, u);
+    TreePiece w;
+    constexpr int kC = kNT / kR;        // threads of a row
+    constexpr int kO = D / kC;          // output channels of a thread
+    const int orow = tid / kC, oc = (tid % kC) * 4;  // its row; channels oc + 32 j ..
+    while (next_piece(p, cur, u, end, w)) {
+        const int row0 = w.mt * p.tile_rows;
+        const int rows = min(kR, w.nodes * p.G - row0);
+        // row tiles of nodes that do not exist in this entry: nothing to do
+        if (rows <= 0) continue;
+        __syncthreads();
+        for (int x = tid; x < kR * D / 4; x += kNT) {
+            const int r = x / (D / 4), c = x % (D / 4) * 4;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const size_t at = q_offset(p, w.e, w.h, row0 + r, D) + c;
+                if constexpr (TYPE == kTreeF32) {
+                    f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
+                } else {
+                    const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at);
+                    f = make_float4(bf16lo(b.x), bf16hi(b.x), bf16lo(b.y), bf16hi(b.y));
+                }
+            }
+            f.x *= p.qscale; f.y *= p.qscale; f.z *= p.qscale; f.w *= p.qscale;
+            *reinterpret_cast<float4*>(sq + r * D + c) = f;
+        }
+        if (tid < kR) { s_m[tid] = -INFINITY; s_l[tid] = 0.f; }
+        float o[kO];
+#pragma unroll
+        for (int j = 0; j < kO; ++j) o[j] = 0.f;
+
+        for (int tile = w.t0; tile < w.t1; ++tile) {
+            const int tok0 = tile * kT;
+            const int ntok = min(kT, w.prefix + w.nodes - tok0);
+            __syncthreads();
+            for (int x = tid; x < kT * D / 4; x += kNT) {
+                const int t = x / (D / 4), c = x % (D / 4) * 4;
+                float4 fk = make_float4(0.f, 0.f, 0.f, 0.f), fv = fk;
+                if (t < ntok) {
+                    const long long row = tree_row(p.at, w.e, w.h, tok0 + t);
+                    fk = load4<TYPE, D>(p.k, p.k_scale, row, c);
+                    fv = load4<TYPE, D>(p.v, p.v_scale, row, c);
+                }
+                *reinterpret_cast<float4*>(sk + t * (D + 4) + c) = fk;
+                *reinterpret_cast<float4*>(sv + t * D + c) = fv;
+            }
+            __syncthreads();
+            // scores: a thread takes one row and tokens t = tid % 8 + 8 j
+            {
+                const int r = tid / kC;
+                float acc[kT / kC] = {};
+                for (int c = 0; c < D; c += 4) {
+                    const float4 a = *reinterpret_cast<const float4*>(sq + r * D + c);
+#pragma unroll
+                    for (int j = 0; j < kT / kC; ++j) {
+                        const float4 b = *reinterpret_cast<const float4*>(sk + (tid % kC + kC * j) * (D + 4) + c);
+                        acc[j] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc[j]))));
+                    }
+                }
+                const int node = (row0 + r) / p.G;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < kT / kC; ++j) {
+                    const int t = tid % kC + kC * j, tok = tok0 + t - w.prefix;  // node index of the token
+                    bool sees = r < rows && t < ntok;
+                    if (sees && tok >= 0) sees = mask_word(p, w.e, node, tok >> 5) >> (tok & 31) & 1;
+                    acc[j] = sees ? acc[j] : -INFINITY;
+                    mx = fmaxf(mx, acc[j]);
+                }
+#pragma unroll
+                for (int x = 1; x < kC; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                const float m_old = s_m[r], m_new = fmaxf(m_old, mx);
+                const float base = m_new == -INFINITY ? 0.f : m_new;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < kT / kC; ++j) {
+                    const float e = exp2f(acc[j] - base);
+                    ss[r * (kT + 4) + tid % kC + kC * j] = e;
+                    sum += e;
+                }
+#pragma unroll
+                for (int x = 1; x < kC; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                __syncwarp();
+                if (tid % kC == 0) {
+                    const float f = exp2f(m_old - base);
+                    s_w[r] = f;
+                    s_l[r] = s_l[r] * f + sum;
+                    s_m[r] = m_new;
+                }
+            }
+            __syncthreads();
+            {
+                const float f = s_w[orow];
+#pragma unroll
+                for (int j = 0; j < kO; ++j) o[j] *= f;
+                for (int t = 0; t < ntok; ++t) {
+                    const float e = ss[orow * (kT + 4) + t];
+                    if (e == 0.f) continue;  // a masked token does not count, whatever its values are
+#pragma unroll
+                    for (int j = 0; j < kO / 4; ++j) {
+                        const float4 v = *reinterpret_cast<const float4*>(sv + t * D + oc + 4 * kC * j);
+                        o[4 * j + 0] = fmaf(e, v.x, o[4 * j + 0]);
+                        o[4 * j + 1] = fmaf(e, v.y, o[4 * j + 1]);
+                        o[4 * j + 2] = fmaf(e, v.z, o[4 * j + 2]);
+                        o[4 * j + 3] = fmaf(e, v.w, o[4 * j + 3]);
+                    }
+                }
+            }
+        }
+        if (orow < rows) {
+            const float l = s_l[orow];
+            if (w.whole()) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const size_t at = q_offset(p, w.e, w.h, row0 + orow, D);
+#pragma unroll
+                for (int j = 0; j < kO; ++j) {
+                    const size_t x = at + oc + 4 * kC * (j / 4) + j % 4;
+                    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[x] = __float2bfloat16_rn(o[j] * inv);
+                    else static_cast<float*>(p.out)[x] = o[j] * inv;
+                }
+            } else {
+                float* part = part_of(p, blockIdx.x, w.t0 == 0, D);
+                if (tid % kC == 0) { part[orow] = s_m[orow]; part[p.part_rows + orow] = l; }
+                float* po = part + 2 * p.part_rows + (size_t)orow * D;
+#pragma unroll
+                for (int j = 0; j < kO; ++j) po[oc + 4 * kC * (j / 4) + j % 4] = o[j];
+            }
+        }
+    }
+}
+
+template <int TYPE, int D>
+cudaError_t run(const TreeParams& p, cudaStream_t st) {
+    static_assert(simt_smem<D>() <= 227 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(ds_tree_simt_kernel<TYPE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         simt_smem<D>());
+    if (e != cudaSuccess) return e;
+    ds_tree_simt_kernel<TYPE, D><<<p.grid, kNT, simt_smem<D>(), st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+TreePlan plan_tree_simt(int rows, int d) {
+    (void)rows; (void)d;
+    return TreePlan{kR, kT, 2 * 148};
+}
+
+cudaError_t launch_tree_simt(const TreeParams& p, int type, int d, cudaStream_t st) {
+    if (type == kTreeF32) return d == 64 ? run<kTreeF32, 64>(p, st) : run<kTreeF32, 128>(p, st);
+    if (type == kTreeBF16) return d == 64 ? run<kTreeBF16, 64>(p, st) : run<kTreeBF16, 128>(p, st);
+    return d == 64 ? run<kTreeE4M3, 64>(p, st) : run<kTreeE4M3, 128>(p, st);
+}
+
+}  // namespace ds

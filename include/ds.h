@@ -66,7 +66,9 @@ typedef enum {
     DS_ERR_TIMEOUT = 5
 } ds_status;
 
-typedef enum { DS_F32 = 0, DS_BF16 = 1, DS_F16 = 2, DS_INT4 = 3 } ds_dtype;
+/* DS_E4M3: 8-bit floats (4 exponent and 3 mantissa bits), a K/V cache type of
+ * the calls in "writing and reading caches" and "drafted trees" only. */
+typedef enum { DS_F32 = 0, DS_BF16 = 1, DS_F16 = 2, DS_INT4 = 3, DS_E4M3 = 4 } ds_dtype;
 
 /* Human-readable name of a status code (static string). */
 DS_API const char* ds_status_string(ds_status st);
@@ -307,6 +309,140 @@ DS_API ds_status ds_decode_step_paged(const void* q, const void* k_pool, const v
                                       int b, int hq, int hkv, int s_max, int s_cap, int d, int c,
                                       int topk, float sm_scale, void* out, ds_dtype out_dt,
                                       int32_t* sel_out, float* score_out, cudaStream_t stream);
+
+/* ------------------------------------------- writing and reading caches
+ * 8-bit caches. A K/V cache of type DS_E4M3 holds one byte a channel (same
+ * layout as the other types) and one fp32 scale a row:
+ *     k_scale, v_scale  [b, hkv, s_cap]  (paged: [num_blocks, hkv, page_size])
+ * A row x (fp32 values) is written as
+ *     scale = max(max_c |x_c| / 448, 2^-126),   code_c = e4m3_rn(x_c / scale)
+ * (IEEE divisions, round to nearest even) and stands for scale * code_c. A row
+ * that holds a NaN or an infinity gets the scale NaN and reads back as NaN
+ * throughout. */
+
+/* Which channels of the first rot_dim rotate together, j < rot_dim / 2. */
+typedef enum {
+    DS_ROPE_HALF = 0,        /* channels j and j + rot_dim / 2 */
+    DS_ROPE_INTERLEAVED = 1  /* channels 2j and 2j + 1 */
+} ds_rope;
+
+/* Writes the keys and values of t new tokens an entry into the caches as the
+ * projections left them: norm of each head, position rotation and (8-bit)
+ * quantisation in the pass that stores them; the queries get the same norm
+ * and rotation and go to q_out. In fp32, for a head's vector x [d] of token i
+ * of entry b:
+ *     y = x * w / sqrt(mean(x^2) + eps)          (only with q_weight / k_weight)
+ *     (y_a, y_c) -> (y_a cos - y_c sin, y_c cos + y_a sin)   for the pairs of
+ *         `rope`, angle = positions[b, i] * inv_freq[j]      (only with inv_freq)
+ * and one rounding to the destination's type. Values are neither normed nor
+ * rotated. The angle is formed and reduced in 64 bits, so far positions lose
+ * nothing. K and V rows go to cache row starts[b] + i; rows outside [0, s_cap)
+ * are not written (their queries still are). Tokens i >= lens[b] are skipped:
+ * neither their queries nor their rows are touched.
+ *   q, k, v     dtype dt (DS_F32 or DS_BF16): head h of token i of entry b
+ *               starts *_bs * b + *_ts * i + d * h elements in (so three views
+ *               of one fused projection work); strides * element size must be
+ *               multiples of 16 bytes. q may be NULL (then q_out is too).
+ *   q_weight, k_weight  [d] dtype dt, or NULL (no norm of that kind)
+ *   inv_freq    [rot_dim / 2] fp32, or NULL (no rotation); rot_dim a multiple
+ *               of 16, at most d
+ *   positions   [b, t] int32, or NULL (starts[b] + i)
+ *   starts      [b] int32, or NULL (0);  lens [b] int32 (clamped into [0, t]),
+ *               or NULL (t)
+ *   q_out       [b, t, hq, d] dtype dt; may be q itself where q has that layout
+ *   k_cache, v_cache  dtype cache_dt: dt, or DS_E4M3 with k_scale and v_scale
+ * Two tokens of one call that go to the same row leave either's contents.
+ * inv_freq, positions, starts, lens and the scales need 4-byte alignment, the
+ * other pointers 16. DS_ERR_UNSUPPORTED for b * t > 2^30 or a cache dtype that
+ * is neither. */
+DS_API ds_status ds_write_kv(const void* q, long long q_bs, long long q_ts,
+                             const void* k, long long k_bs, long long k_ts,
+                             const void* v, long long v_bs, long long v_ts, ds_dtype dt,
+                             const void* q_weight, const void* k_weight, float eps,
+                             const float* inv_freq, int rot_dim, ds_rope rope,
+                             const int32_t* positions, const int32_t* starts, const int32_t* lens,
+                             int b, int t, int hq, int hkv, int s_cap, int d, void* q_out,
+                             void* k_cache, void* v_cache, ds_dtype cache_dt,
+                             float* k_scale, float* v_scale, cudaStream_t stream);
+
+/* ds_write_kv into paged pools [num_blocks, hkv, page_size, d] (see "paged
+ * K/V" for the rules of block_table). Cache rows run to max_blocks *
+ * page_size; a row whose block id is outside [0, num_blocks) is not written. */
+DS_API ds_status ds_write_kv_paged(const void* q, long long q_bs, long long q_ts,
+                                   const void* k, long long k_bs, long long k_ts,
+                                   const void* v, long long v_bs, long long v_ts, ds_dtype dt,
+                                   const void* q_weight, const void* k_weight, float eps,
+                                   const float* inv_freq, int rot_dim, ds_rope rope,
+                                   const int32_t* positions, const int32_t* starts, const int32_t* lens,
+                                   int b, int t, int hq, int hkv, int d, void* q_out,
+                                   void* k_pool, void* v_pool, ds_dtype cache_dt,
+                                   float* k_scale, float* v_scale, const int32_t* block_table,
+                                   int max_blocks, int page_size, int num_blocks, cudaStream_t stream);
+
+/* Reads rows [0, s) of an 8-bit cache back: out = scale * code, rounded once
+ * to out_dt (DS_F32 or DS_BF16), into k_out, v_out [b, hkv, s_out_cap, d], the
+ * layout that ds_build_label_cache and the decode calls read. seq_lens [b]
+ * (int32, clamped into [0, s]; or NULL) gives each entry's own row count; rows
+ * past it, and rows past s, are not touched. The v triple (v_cache, v_scale,
+ * v_out) may be NULL together: only the keys are read then. */
+DS_API ds_status ds_read_kv(const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, const int32_t* seq_lens, int b, int hkv, int s,
+                            int s_cap, int d, void* k_out, void* v_out, ds_dtype out_dt,
+                            int s_out_cap, cudaStream_t stream);
+
+/* ds_read_kv from paged pools; block ids are clamped into the pool. */
+DS_API ds_status ds_read_kv_paged(const void* k_pool, const void* v_pool, const float* k_scale,
+                                  const float* v_scale, const int32_t* block_table, int max_blocks,
+                                  int page_size, int num_blocks, const int32_t* seq_lens,
+                                  int b, int hkv, int s, int d, void* k_out, void* v_out,
+                                  ds_dtype out_dt, int s_out_cap, cudaStream_t stream);
+
+/* --------------------------------------------------------- drafted trees
+ * Attention of t drafted tokens an entry (a tree; t = 1 is one ordinary
+ * decode token) over a cache that already holds their K/V rows: entry b has a
+ * prefix of p_b tokens in rows [0, p_b) and its node j in row p_b + j. Node i
+ * sees the whole prefix and the nodes j that its mask shows:
+ *     out[b, i, h] = softmax(sm_scale * q[b, i, h] . k[b, g, r]) . v[b, g, r]
+ * over those rows r, g = h / (hq / hkv). What a node does not see does not
+ * count, whatever it holds (NaN and infinities too). A node that sees nothing
+ * gets zeros.
+ *   q, out     [b, t, hq, d]; q of dtype DS_F32 with a DS_F32 cache, else
+ *              DS_BF16; out DS_F32, or DS_BF16 where q is
+ *   k, v       dtype kvdt: DS_F32, DS_BF16, or DS_E4M3 with k_scale, v_scale
+ *   mask       [b, t, ceil(t / 32)] int32: bit j % 32 of word j / 32 of row i
+ *              shows node j to node i (bits from t on are ignored); or NULL:
+ *              a chain, node i sees nodes 0 .. i
+ *   seq_lens   [b] int32, p_b clamped into [0, s]; or NULL (s)
+ *   node_lens  [b] int32, each entry's own number of nodes, clamped into
+ *              [0, t]; or NULL (t). Nodes past it are seen by none, and their
+ *              rows of out are not touched.
+ *   s          0 <= s, s + t <= s_cap;  1 <= t <= 256
+ *   sm_scale   <= 0 selects 1/sqrt(d)
+ *   ws         device scratch of ds_tree_decode_workspace_size() bytes, 16-byte
+ *              aligned, whose contents on entry do not matter. Calls that may
+ *              run at the same time need their own.
+ * Scores, softmax statistics and sums are fp32. With bf16 and 8-bit caches the
+ * products run on the tensor cores, and a weight exp(.) (times its row's
+ * v_scale) is rounded to bf16 before its product with v. mask, seq_lens,
+ * node_lens and the scales need 4-byte alignment, the other pointers 16. */
+DS_API ds_status ds_tree_decode_workspace_size(int b, int t, int hq, int hkv, int s, int d,
+                                               ds_dtype kvdt, size_t* bytes);
+DS_API ds_status ds_tree_decode(const void* q, const void* k, const void* v, ds_dtype kvdt,
+                                const float* k_scale, const float* v_scale, const int32_t* mask,
+                                const int32_t* seq_lens, const int32_t* node_lens, int b, int t,
+                                int hq, int hkv, int s, int s_cap, int d, float sm_scale, void* out,
+                                ds_dtype out_dt, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ds_tree_decode over paged pools [num_blocks, hkv, page_size, d] (see "paged
+ * K/V"; s + t <= max_blocks * page_size). Same results as the dense layout
+ * on the same values. */
+DS_API ds_status ds_tree_decode_paged(const void* q, const void* k_pool, const void* v_pool,
+                                      ds_dtype kvdt, const float* k_scale, const float* v_scale,
+                                      const int32_t* mask, const int32_t* block_table, int max_blocks,
+                                      int page_size, int num_blocks, const int32_t* seq_lens,
+                                      const int32_t* node_lens, int b, int t, int hq, int hkv, int s,
+                                      int d, float sm_scale, void* out, ds_dtype out_dt, void* ws,
+                                      size_t ws_bytes, cudaStream_t stream);
 
 /* Launch plan of ds_sparse_decode for a shape (host only, launches nothing),
  * for caches of capacity s on a 148-SM B200: CTAs per thread-block cluster
