@@ -34,7 +34,7 @@ struct TreeParams {
     void* out;
     int out_bf16;
     float* part;     // partial results: see part_of
-    int part_rows;   // rows of a partial: min(rows, tile_rows)
+    int part_rows;   // rows of a partial: min(rows, tile_rows), rounded up to a multiple of 4
     unsigned int* err;
 };
 
@@ -184,10 +184,13 @@ __device__ __forceinline__ long long tree_row(const CacheRows& c, int e, int h, 
 
 enum TreeType { kTreeF32 = 0, kTreeBF16 = 1, kTreeE4M3 = 2 };
 
-// Launches (ds_tree_simt.cu, ds_tree_combine.cu).
+// Launches. f32 (ds_tree_simt.cu):
 struct TreePlan { int tile_rows, tile_tokens, grid; };
 TreePlan plan_tree_simt(int rows, int d);
-cudaError_t launch_tree_simt(const TreeParams& p, int type, int d, cudaStream_t st);
+cudaError_t launch_tree_simt(const TreeParams& p, int d, cudaStream_t st);
+// bf16 and e4m3 (ds_tree_tc.cu).
+TreePlan plan_tree_tc(int rows, int d);
+cudaError_t launch_tree_tc(const TreeParams& p, int type, int d, cudaStream_t st);
 cudaError_t launch_tree_combine(const TreeParams& p, int d, cudaStream_t st);
 
 }  // namespace ds

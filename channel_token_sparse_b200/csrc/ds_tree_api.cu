@@ -148,13 +148,14 @@ ds_status tree_shape(int b, int t, int hq, int hkv, int s, int d, ds_dtype kvdt,
         DS_FAIL(DS_ERR_UNSUPPORTED, "k/v dtype %d (supported: f32, bf16, e4m3)", (int)kvdt);
     o->type = kvdt == DS_F32 ? ds::kTreeF32 : kvdt == DS_BF16 ? ds::kTreeBF16 : ds::kTreeE4M3;
     const int rows = t * (hq / hkv);
-    o->plan = ds::plan_tree_simt(rows, d);
+    o->plan = o->type == ds::kTreeF32 ? ds::plan_tree_simt(rows, d) : ds::plan_tree_tc(rows, d);
     o->n_mt = (rows + o->plan.tile_rows - 1) / o->plan.tile_rows;
-    o->part_rows = rows < o->plan.tile_rows ? rows : o->plan.tile_rows;
+    // a multiple of 4 keeps every place, and the values behind its rows' statistics, 16-byte aligned
+    o->part_rows = ((rows < o->plan.tile_rows ? rows : o->plan.tile_rows) + 3) / 4 * 4;
     const long long units = (long long)b * hkv * o->n_mt * (((long long)s + t + o->plan.tile_tokens - 1) / o->plan.tile_tokens);
     o->grid = units < o->plan.grid ? (int)units : o->plan.grid;
-    // two places a CTA for pieces of split items (rounded up to 16 bytes)
-    o->ws = ((size_t)o->grid * 2 * o->part_rows * (d + 2) * 4 + 15) / 16 * 16;
+    // two places a CTA for pieces of split items
+    o->ws = (size_t)o->grid * 2 * o->part_rows * (d + 2) * 4;
     return DS_OK;
 }
 
@@ -190,7 +191,9 @@ ds_status tree_decode(const void* q, const void* k, const void* v, ds_dtype kvdt
     p.qscale = (sm_scale > 0.f ? sm_scale : 1.0f / sqrtf((float)d)) * 1.4426950408889634f;
     p.out = out; p.out_bf16 = out_dt == DS_BF16;
     p.part = static_cast<float*>(ws);
-    cudaError_t e = ds::launch_tree_simt(p, sh.type, d, stream);
+    cudaError_t e = ds::device_status_word(&p.err);
+    if (e != cudaSuccess) return launched(e, "cudaGetSymbolAddress");
+    e = sh.type == ds::kTreeF32 ? ds::launch_tree_simt(p, d, stream) : ds::launch_tree_tc(p, sh.type, d, stream);
     if (e == cudaSuccess) e = ds::launch_tree_combine(p, d, stream);
     return launched(e, "tree decode launch");
 }

@@ -1,9 +1,9 @@
-// ds_tree_simt.cu -- tree attention with fp32 arithmetic on the CUDA cores.
+// ds_tree_simt.cu -- tree attention over fp32 caches, on the CUDA cores.
 //
 // One pass over an item's tokens with the running maximum and sum of each
 // row's softmax: for a tile of 64 tokens the scores s = qscale * q.k (base-2
 // exponents) of 32 query rows, their new maxima, weights 2^(s - m), and the
-// weighted values, all in fp32. A tile's K and V rows are converted to fp32 in
+// weighted values, all in fp32. A tile's K and V rows are read into
 // shared memory once and serve the 32 rows.
 #include <math.h>
 
@@ -17,32 +17,9 @@ constexpr int kNT = 256;
 constexpr int kR = 32;     // query rows of a row tile
 constexpr int kT = 64;     // tokens of a token tile
 
-__device__ __forceinline__ float e4m3_lo(uint32_t w, int j) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * (j >> 1)))));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return (j & 1) ? f.y : f.x;
-}
-
-// Four consecutive channels of cache row `row`, times its scale.
-template <int TYPE, int D>
-__device__ __forceinline__ float4 load4(const void* base, const float* scale, long long row, int c) {
-    if constexpr (TYPE == kTreeF32) {
-        const uint4 w = ldg_stream16(static_cast<const float*>(base) + row * D + c);
-        return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-    } else if constexpr (TYPE == kTreeBF16) {
-        const uint2 w = ldg_stream8(static_cast<const uint16_t*>(base) + row * D + c);
-        return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-    } else {
-        const uint32_t w = ldg_stream4(static_cast<const uint8_t*>(base) + row * D + c);
-        const float sc = __ldg(scale + row);
-        return make_float4(e4m3_lo(w, 0) * sc, e4m3_lo(w, 1) * sc, e4m3_lo(w, 2) * sc, e4m3_lo(w, 3) * sc);
-    }
-}
-
 template <int D> constexpr int simt_smem() { return (kR * D + kT * (D + 4) + kT * D + kR * (kT + 4) + 3 * kR) * 4; }
 
-template <int TYPE, int D>
+template <int D>
 __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const TreeParams p) {
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;                     // [kR][D] queries, times qscale
@@ -75,12 +52,7 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const TreeParams p) {
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const size_t at = q_offset(p, w.e, w.h, row0 + r, D) + c;
-                if constexpr (TYPE == kTreeF32) {
-                    f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
-                } else {
-                    const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at);
-                    f = make_float4(bf16lo(b.x), bf16hi(b.x), bf16lo(b.y), bf16hi(b.y));
-                }
+                f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
             }
             f.x *= p.qscale; f.y *= p.qscale; f.z *= p.qscale; f.w *= p.qscale;
             *reinterpret_cast<float4*>(sq + r * D + c) = f;
@@ -99,8 +71,8 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const TreeParams p) {
                 float4 fk = make_float4(0.f, 0.f, 0.f, 0.f), fv = fk;
                 if (t < ntok) {
                     const long long row = tree_row(p.at, w.e, w.h, tok0 + t);
-                    fk = load4<TYPE, D>(p.k, p.k_scale, row, c);
-                    fv = load4<TYPE, D>(p.v, p.v_scale, row, c);
+                    fk = *reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row * D + c);
+                    fv = *reinterpret_cast<const float4*>(static_cast<const float*>(p.v) + row * D + c);
                 }
                 *reinterpret_cast<float4*>(sk + t * (D + 4) + c) = fk;
                 *reinterpret_cast<float4*>(sv + t * D + c) = fv;
@@ -176,8 +148,7 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const TreeParams p) {
 #pragma unroll
                 for (int j = 0; j < kO; ++j) {
                     const size_t x = at + oc + 4 * kC * (j / 4) + j % 4;
-                    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[x] = __float2bfloat16_rn(o[j] * inv);
-                    else static_cast<float*>(p.out)[x] = o[j] * inv;
+                    static_cast<float*>(p.out)[x] = o[j] * inv;
                 }
             } else {
                 float* part = part_of(p, blockIdx.x, w.t0 == 0, D);
@@ -190,13 +161,13 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const TreeParams p) {
     }
 }
 
-template <int TYPE, int D>
+template <int D>
 cudaError_t run(const TreeParams& p, cudaStream_t st) {
     static_assert(simt_smem<D>() <= 227 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(ds_tree_simt_kernel<TYPE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(ds_tree_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          simt_smem<D>());
     if (e != cudaSuccess) return e;
-    ds_tree_simt_kernel<TYPE, D><<<p.grid, kNT, simt_smem<D>(), st>>>(p);
+    ds_tree_simt_kernel<D><<<p.grid, kNT, simt_smem<D>(), st>>>(p);
     return cudaGetLastError();
 }
 
@@ -207,10 +178,8 @@ TreePlan plan_tree_simt(int rows, int d) {
     return TreePlan{kR, kT, 2 * 148};
 }
 
-cudaError_t launch_tree_simt(const TreeParams& p, int type, int d, cudaStream_t st) {
-    if (type == kTreeF32) return d == 64 ? run<kTreeF32, 64>(p, st) : run<kTreeF32, 128>(p, st);
-    if (type == kTreeBF16) return d == 64 ? run<kTreeBF16, 64>(p, st) : run<kTreeBF16, 128>(p, st);
-    return d == 64 ? run<kTreeE4M3, 64>(p, st) : run<kTreeE4M3, 128>(p, st);
+cudaError_t launch_tree_simt(const TreeParams& p, int d, cudaStream_t st) {
+    return d == 64 ? run<64>(p, st) : run<128>(p, st);
 }
 
 }  // namespace ds
