@@ -51,6 +51,17 @@ __device__ __forceinline__ int item_units(const TreeParams& p, int e) {
     return n > 0 ? (tree_prefix(p, e) + n + p.tile_tokens - 1) / p.tile_tokens : 0;
 }
 
+// Units before entry e (called by whole warps).
+__device__ __forceinline__ long long tree_before(const TreeParams& p, int e) {
+    const long long per = (long long)p.hkv * p.n_mt;
+    if (!p.seq_lens && !p.node_lens) return (long long)item_units(p, 0) * per * e;
+    long long sum = 0;
+    for (int x = lane_id(); x < e; x += 32) sum += item_units(p, x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum * per;
+}
+
 // A place in the order of units. Every member is the same in all lanes.
 struct TreeCursor {
     int e = 0;                // entry
@@ -67,18 +78,7 @@ __device__ __forceinline__ void cursor_entry(const TreeParams& p, TreeCursor& c,
 }
 
 // Units of the whole call (called by whole warps).
-__device__ __forceinline__ long long tree_total(const TreeParams& p) {
-    const long long per = (long long)p.hkv * p.n_mt;
-    if (!p.seq_lens && !p.node_lens) return (long long)item_units(p, 0) * per * p.b;
-    long long sum = 0;
-    for (int e0 = 0; e0 < p.b; e0 += 32) {
-        const int e = e0 + lane_id();
-        sum += e < p.b ? item_units(p, e) : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum * per;
-}
+__device__ __forceinline__ long long tree_total(const TreeParams& p) { return tree_before(p, p.b); }
 
 // The cursor whose entry holds unit u < total (called by whole warps).
 __device__ __forceinline__ TreeCursor tree_seek(const TreeParams& p, long long u) {
@@ -86,7 +86,7 @@ __device__ __forceinline__ TreeCursor tree_seek(const TreeParams& p, long long u
     TreeCursor c;
     if (!p.seq_lens && !p.node_lens) {
         const long long n = (long long)item_units(p, 0) * per;
-        const int e = (int)(u / n);
+        const int e = (int)((u | n) >> 31 ? u / n : (long long)((unsigned)u / (unsigned)n));
         c.base = (long long)e * n;
         cursor_entry(p, c, e);
         return c;
@@ -115,8 +115,33 @@ __device__ __forceinline__ TreeCursor tree_seek(const TreeParams& p, long long u
     return c;
 }
 
-// First unit of CTA i's share (share i ends where share i + 1 begins).
-__device__ __forceinline__ long long share_begin(long long total, int i, int grid) { return total * i / grid; }
+// The shares of `grid` CTAs of `total` units: the first `extra` have one more
+// than the others' `each`.
+struct TreeShares {
+    long long each;
+    int extra;
+    __device__ __forceinline__ TreeShares(long long total, int grid) {
+        if (total >> 31) {
+            each = total / grid;
+            extra = (int)(total - each * grid);
+        } else {
+            const unsigned q = (unsigned)total / (unsigned)grid;
+            each = q;
+            extra = (int)((unsigned)total - q * (unsigned)grid);
+        }
+    }
+    // First unit of CTA i's share (share i ends where share i + 1 begins).
+    __device__ __forceinline__ long long begin(int i) const { return each * i + min(i, extra); }
+    // The CTA whose share holds unit u.
+    __device__ __forceinline__ int holder(long long u) const {
+        const long long wide = (each + 1) * extra;
+        if (u < wide) return (int)quotient(u, each + 1);
+        return extra + (int)quotient(u - wide, each);
+    }
+    static __device__ __forceinline__ long long quotient(long long a, long long b) {
+        return (a | b) >> 31 ? a / b : (long long)((unsigned)a / (unsigned)b);
+    }
+};
 
 // A CTA's piece of one item.
 struct TreePiece {
@@ -137,7 +162,7 @@ __device__ __forceinline__ bool next_piece(const TreeParams& p, TreeCursor& c, l
         cursor_entry(p, c, c.e + 1);
     }
     const long long in_entry = u - c.base;
-    const int item = (int)(in_entry / c.units);
+    const int item = (int)TreeShares::quotient(in_entry, c.units);
     w.e = c.e; w.h = item / p.n_mt; w.mt = item - w.h * p.n_mt;
     w.prefix = c.prefix; w.nodes = c.nodes; w.units = c.units;
     w.t0 = (int)(in_entry - (long long)item * c.units);

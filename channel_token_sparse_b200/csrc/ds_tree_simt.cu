@@ -20,7 +20,7 @@ constexpr int kT = 64;     // tokens of a token tile
 template <int D> constexpr int simt_smem() { return (kR * D + kT * (D + 4) + kT * D + kR * (kT + 4) + 3 * kR) * 4; }
 
 template <int D>
-__global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;                     // [kR][D] queries, times qscale
     float* sk = sq + kR * D;            // [kT][D + 4]
@@ -32,9 +32,9 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const TreeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int tid = threadIdx.x;
-    const long long total = tree_total(p);
-    long long u = share_begin(total, blockIdx.x, p.grid);
-    const long long end = share_begin(total, blockIdx.x + 1, p.grid);
+    const TreeShares shares(tree_total(p), p.grid);
+    long long u = shares.begin(blockIdx.x);
+    const long long end = shares.begin(blockIdx.x + 1);
     if (u >= end) return;
     TreeCursor cur = tree_seek(p, u);
     TreePiece w;

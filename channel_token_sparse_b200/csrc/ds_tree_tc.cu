@@ -14,7 +14,7 @@
 // and both use every token tile, which halves the reads a row costs.
 //
 // Roles: warps 0-3 and 4-7 softmax of stream 0 and 1 (a thread a row), warp 8
-// issues the products, the others bring K and V tiles into a ring of
+// issues the products, warps 12 on bring K and V tiles into a ring of
 // 128-byte-swizzled stages by 16-byte asynchronous copies (any page size;
 // rows past the sequence become zeros). 8-bit tiles are copied as they are
 // into the loaders' own slots, widened to bf16 (exact) and stored into the
@@ -23,7 +23,8 @@
 // The products take every row of V with every weight, and 0 * NaN is NaN, so
 // the rows of tree nodes (which some query rows may not see) are looked
 // through for values that are not finite; such values are zeroed in the stage
-// and added to the rows that do see them at the end.
+// and added to the rows that do see them at the end. An 8-bit tree row whose
+// scales are not finite is set aside the same way.
 #include <math.h>
 
 #include "ds_tree.cuh"
@@ -38,7 +39,12 @@ template <int TYPE, int D, int MT>
 struct Cfg {
     static constexpr bool kQ8 = TYPE == kTreeE4M3;
     static constexpr int kLoadWarps = kQ8 ? 8 : 4;
-    static constexpr int kThreads = (9 + kLoadWarps) * 32;
+    static constexpr int kThreads = (12 + kLoadWarps) * 32;
+    // Registers of a thread by role: 512 (8-bit: 640) threads are launched with
+    // 128 (96) each, and the four-warp groups redistribute them: their sums are
+    // 168 + 168 + 72 + 104 = 4 * 128 and 136 + 136 + 64 + 2 * 72 = 5 * 96.
+    static constexpr int kRegSoftmax = kQ8 ? 136 : 168, kRegMma = kQ8 ? 64 : 72, kRegLoad = kQ8 ? 72 : 104;
+    static_assert(2 * kRegSoftmax + kRegMma + (kQ8 ? 2 : 1) * kRegLoad <= (kQ8 ? 5 * 96 : 4 * 128), "registers");
     static constexpr int kStage = kT * D * 2;       // bytes of a K or V tile in bf16
     static constexpr int kQ = MT * kT * D * 2;
     static constexpr int kRaw = kQ8 ? (D == 128 ? 3 : 6) : 0;
@@ -112,6 +118,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                  " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
                  ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
 }
+// One lane of the warp, the same one every time.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -126,7 +140,9 @@ struct Waiter {
     volatile int* stop;
     unsigned int* err;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-        if (mbar_try_wait(bar, parity)) return true;
+        return mbar_try_wait(bar, parity) || poll(bar, parity);
+    }
+    __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) const {
         const uint64_t t0 = global_ns();
         for (;;) {
             for (int i = 0; i < 64; ++i)
@@ -147,6 +163,11 @@ template <int N> struct Ring {
     __device__ __forceinline__ void next() { if (++i == N) { i = 0; ph ^= 1; } }
 };
 
+// 16 bytes from global to shared memory, or 16 zero bytes (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0));
+}
+
 // Byte offset of 16-byte chunk c (eight channels) of row r in a tile: blocks
 // of 64 channels, rows of 128 bytes, chunks exchanged within groups of 8 rows.
 __device__ __forceinline__ int tile_at(int r, int c) { return (c >> 3) * (kT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
@@ -165,38 +186,59 @@ __device__ __forceinline__ uint32_t visible(const TreeParams& p, int e, int node
     return sh ? word(w) >> sh | word(w + 1) << (32 - sh) : word(w);
 }
 
-// Four e4m3 codes -> four bf16 values (exact).
+// Four e4m3 codes -> four bf16 values (exact). A code's sign, exponent and
+// mantissa bits at their places in a bf16 are its value times 2^-120 (the
+// difference of the exponents' biases, subnormals too); the product with 2^120
+// is exact. (The conversion instructions bounded 8-bit tiles.) The NaN code
+// becomes +-480: rows that are not finite are marked by their scale.
+__device__ __forceinline__ uint32_t widen2(uint32_t x) {  // codes in the halves' high bytes
+    uint32_t r = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x7b807b80u));
+    return r;
+}
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
-    uint32_t a, b;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)w));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(w >> 16)));
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    return make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y));
+    return make_uint2(widen2(__byte_perm(w, 0, 0x1404)), widen2(__byte_perm(w, 0, 0x3424)));
 }
 
-// The order in which a piece of n token tiles uses the ring. MT = 1: K0 K1,
-// then V_i K_{i+2}; MT = 2: K_i V_i. Calls f(token tile, is V).
-template <int MT, typename F>
-__device__ __forceinline__ bool ring_order(int n, F f) {
-    if (MT == 1) {
-        if (!f(0, false)) return false;
-        if (n > 1 && !f(1, false)) return false;
-        for (int i = 0; i < n; ++i) {
-            if (!f(i, true)) return false;
-            if (i + 2 < n && !f(i + 2, false)) return false;
-        }
-    } else {
-        for (int i = 0; i < n; ++i)
-            if (!f(i, false) || !f(i, true)) return false;
+// The pages of a token tile: a lane keeps the block of the tile's rows 4 lane
+// .. 4 lane + 3, so one table read a warp and tile serves its 128 rows. Pages
+// of one or two rows are looked up row by row.
+struct TilePages {
+    int blk = 0;
+    __device__ __forceinline__ void load(const CacheRows& c, int e, int tok0, int tokens) {
+        if (c.page_shift < 2) return;
+        const int t = min(tok0 + 4 * lane_id(), tokens - 1);
+        blk = __ldg(c.block_table + (size_t)e * c.max_blocks + (t >> c.page_shift));
+        blk = min(max(blk, 0), c.num_blocks - 1);
     }
-    return true;
+    // Pool row of token t = tok0 + r < tokens (called by whole warps).
+    __device__ __forceinline__ long long row(const CacheRows& c, int e, int h, int t, int r) const {
+        if (c.page_shift < 2) return tree_row(c, e, h, t);
+        const int b = __shfl_sync(0xffffffffu, blk, r >> 2);
+        return (((long long)b * c.hkv + h) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+    }
+};
+
+// The order in which a piece of n token tiles uses the ring: the k-th of its
+// 2n uses is token tile `i`, of V or K. MT = 1: K0 K1, then V_i K_{i+2};
+// MT = 2: K_i V_i.
+struct RingUse { int i; bool is_v; };
+template <int MT> __device__ __forceinline__ RingUse ring_use(int k, int n) {
+    if (MT == 2) return RingUse{k >> 1, (k & 1) != 0};
+    const int lead = n > 1 ? 2 : 1, j = k - lead;
+    if (j < 0) return RingUse{k, false};
+    if (j < 2 * (n - 2)) return RingUse{(j & 1) ? 2 + j / 2 : j / 2, (j & 1) == 0};
+    return RingUse{k - n, true};  // the last V tiles
+}
+// The use of the ring that holds V of token tile i.
+template <int MT> __device__ __forceinline__ int v_use(int i, int n) {
+    return MT == 2 ? 2 * i + 1 : n == 1 ? 1 : i < n - 1 ? 2 * i + 2 : 2 * i + 1;
 }
 
 // -------------------------------------------------------------------- kernel
 
 template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kernel(const __grid_constant__ TreeParams p) {
     using C = Cfg<TYPE, D, MT>;
     constexpr int NS = C::kStages;
     constexpr int kChunks = D / 8;  // 16-byte chunks of a bf16 row
@@ -244,58 +286,67 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
     const uint32_t tmem = *tmem_slot;
     const Waiter wait{stop, p.err};
 
-    const long long total = tree_total(p);
-    long long u = share_begin(total, blockIdx.x, p.grid);
-    const long long end = share_begin(total, blockIdx.x + 1, p.grid);
+    const TreeShares shares(tree_total(p), p.grid);
+    long long u = shares.begin(blockIdx.x);
+    const long long end = shares.begin(blockIdx.x + 1);
     TreeCursor cur;
     if (u < end) cur = tree_seek(p, u);
     TreePiece w;
 
-    if (warp >= 9) {
+    if (warp >= 12) {
         // ------------------------------------------------------------ loaders
-        const int tid = threadIdx.x - 9 * 32;
+        reg_dec<C::kRegLoad>();
+        const int tid = threadIdx.x - 12 * 32;
         Ring<NS> ring;
         uint32_t q_ph = 1;  // the first wait on q_empty passes
         if constexpr (!C::kQ8) {
             const int c = tid % kChunks, r0 = tid / kChunks;
             constexpr int kStep = 128 / kChunks;  // rows the 128 threads cover at a time
-            bool ok = true;
-            while (ok && next_piece(p, cur, u, end, w)) {
+            while (next_piece(p, cur, u, end, w)) {
                 const int row0 = w.mt * p.tile_rows, rows = w.nodes * p.G - row0;
                 if (rows <= 0) continue;
-                const int tokens = w.prefix + w.nodes;
-                bool first = true;
-                ok = ring_order<MT>(w.t1 - w.t0, [&](int i, bool is_v) {
-                    if (first) {  // the queries go with the first K tile
-                        first = false;
-                        if (!wait(q_empty, q_ph)) return false;
-                        q_ph ^= 1;
-                        for (int b = 0; b < MT; ++b)
+                const int n = w.t1 - w.t0, tokens = w.prefix + w.nodes;
+                // the queries come with the first K tile
+                if (!__all_sync(0xffffffffu, wait(q_empty, q_ph))) break;
+                q_ph ^= 1;
 #pragma unroll 4
-                            for (int k = 0; k < kChunks; ++k) {
-                                const int r = r0 + k * kStep, row = b * kT + r;
-                                const bool there = row < rows;
-                                const size_t at = there ? q_offset(p, w.e, w.h, row0 + row, D) : 0;
-                                cp_async16_zfill(smem + b * kT * D * 2 + tile_at(r, c),
-                                                 static_cast<const uint16_t*>(p.q) + at + c * 8, there);
-                            }
-                    }
-                    if (!wait(empty + ring.i, ring.ph ^ 1)) return false;
-                    uint8_t* dst = smem + C::oStage + ring.i * C::kStage;
-                    const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v : p.k) + c * 8;
-                    const int tok0 = (w.t0 + i) * kT;
+                for (int k = 0; k < MT * kChunks; ++k) {
+                    const int row = r0 + k * kStep;
+                    const bool there = row < rows;
+                    const size_t at = there ? q_offset(p, w.e, w.h, row0 + row, D) : 0;
+                    cp_async16_zfill(smem + (row / kT) * kT * D * 2 + tile_at(row % kT, c),
+                                     static_cast<const uint16_t*>(p.q) + at + c * 8, there);
+                }
+                bool ok = true;
+                TilePages pages;
+                if (p.at.block_table) pages.load(p.at, w.e, w.t0 * kT, tokens);
+                for (int k = 0; k < 2 * n; ++k) {
+                    const RingUse use = ring_use<MT>(k, n);
+                    ok = __all_sync(0xffffffffu, wait(empty + ring.i, ring.ph ^ 1));
+                    if (!ok) break;
+                    const uint32_t dst = smem_u32(smem + C::oStage + ring.i * C::kStage);
+                    const uint16_t* src = static_cast<const uint16_t*>(use.is_v ? p.v : p.k) + c * 8;
+                    const int tok0 = (w.t0 + use.i) * kT;
+                    if (!p.at.block_table) {
+                        // one run of rows: constant steps from the first
+                        src += (((long long)w.e * p.at.hkv + w.h) * p.at.s_cap + tok0 + r0) * D;
 #pragma unroll
-                    for (int k = 0; k < kChunks; ++k) {
-                        const int r = r0 + k * kStep;
-                        const bool there = tok0 + r < tokens;
-                        const long long row = there ? tree_row(p.at, w.e, w.h, tok0 + r) : 0;
-                        cp_async16_zfill(dst + tile_at(r, c), src + row * D, there);
+                        for (int x = 0; x < kChunks; ++x)
+                            copy16(dst + tile_at(r0 + x * kStep, c), src + x * kStep * D, tok0 + r0 + x * kStep < tokens);
+                    } else {
+#pragma unroll 8
+                        for (int x = 0; x < kChunks; ++x) {
+                            const int r = r0 + x * kStep, t = min(tok0 + r, tokens - 1);
+                            const long long row = pages.row(p.at, w.e, w.h, t, r);
+                            copy16(dst + tile_at(r, c), src + row * D, tok0 + r < tokens);
+                        }
+                        if (k + 1 < 2 * n) pages.load(p.at, w.e, (w.t0 + ring_use<MT>(k + 1, n).i) * kT, tokens);
                     }
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + ring.i))
                                  : "memory");
                     ring.next();
-                    return true;
-                });
+                }
+                if (!ok) break;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
@@ -310,75 +361,64 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             TreePiece aw;
             int a_n = 0, a_k = 0, a_slot = 0;  // tiles of its piece, place in their order, slot
             bool a_more = true;
-            auto a_next = [&](int& i, bool& is_v) {  // the next tile in ring order
-                for (;;) {
-                    if (a_k < 2 * a_n) break;
-                    if (!a_more || !next_piece(p, acur, au, end, aw)) { a_more = false; return false; }
-                    if (aw.nodes * p.G - aw.mt * p.tile_rows <= 0) continue;
-                    a_n = aw.t1 - aw.t0;
-                    a_k = 0;
-                }
-                const int k = a_k++;
-                if (MT == 2) { i = k >> 1; is_v = k & 1; return true; }
-                // K0 K1 V0 K2 V1 K3 ... V_{n-2} V_{n-1}; one tile: K0 V0
-                if (k < 2 && k < a_n) { i = k; is_v = false; return true; }
-                const int j = k - (a_n > 1 ? 2 : 1);  // V0 K2 V1 K3 ...
-                if (j < 2 * (a_n - 2)) { i = (j & 1) ? 2 + j / 2 : j / 2; is_v = !(j & 1); return true; }
-                i = a_n - (2 * a_n - k);
-                is_v = true;
-                return true;
-            };
+            TilePages pages;  // of the next tile to copy
             auto issue = [&] {
-                int i;
-                bool is_v;
-                if (a_next(i, is_v)) {
-                    const int tok0 = (aw.t0 + i) * kT, tokens = aw.prefix + aw.nodes;
-                    const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v : p.k) + c * 16;
-#pragma unroll
-                    for (int k = 0; k < kMine; ++k) {
-                        const int r = r0 + k * kStep;
-                        const bool there = tok0 + r < tokens;
-                        const long long row = there ? tree_row(p.at, aw.e, aw.h, tok0 + r) : 0;
-                        cp_async16_zfill(raw + a_slot * C::kRawBytes + k * 4096, src + row * D, there);
+                while (a_more && a_k >= 2 * a_n) {  // the next piece with rows
+                    a_more = next_piece(p, acur, au, end, aw);
+                    if (a_more && aw.nodes * p.G - aw.mt * p.tile_rows > 0) {
+                        a_n = aw.t1 - aw.t0;
+                        a_k = 0;
+                        if (p.at.block_table) pages.load(p.at, aw.e, aw.t0 * kT, aw.prefix + aw.nodes);
                     }
+                }
+                if (a_more) {
+                    const RingUse use = ring_use<MT>(a_k++, a_n);
+                    const int tok0 = (aw.t0 + use.i) * kT, tokens = aw.prefix + aw.nodes;
+                    const uint8_t* src = static_cast<const uint8_t*>(use.is_v ? p.v : p.k) + c * 16;
+                    const uint32_t dst = smem_u32(raw + a_slot * C::kRawBytes);
+#pragma unroll
+                    for (int x = 0; x < kMine; ++x) {
+                        const int r = r0 + x * kStep, t = min(tok0 + r, tokens - 1);
+                        const long long row = p.at.block_table ? pages.row(p.at, aw.e, aw.h, t, r)
+                                                               : ((long long)aw.e * p.at.hkv + aw.h) * p.at.s_cap + t;
+                        copy16(dst + x * 4096, src + row * D, tok0 + r < tokens);
+                    }
+                    if (p.at.block_table && a_k < 2 * a_n)
+                        pages.load(p.at, aw.e, (aw.t0 + ring_use<MT>(a_k, a_n).i) * kT, tokens);
                 }
                 cp_async_commit();
                 if (++a_slot == C::kRaw) a_slot = 0;
             };
-#pragma unroll
             for (int k = 0; k < C::kRaw - 1; ++k) issue();
             int slot = 0;
-            bool ok = true;
-            while (ok && next_piece(p, cur, u, end, w)) {
+            while (next_piece(p, cur, u, end, w)) {
                 const int row0 = w.mt * p.tile_rows, rows = w.nodes * p.G - row0;
                 if (rows <= 0) continue;
-                bool first = true;
-                ok = ring_order<MT>(w.t1 - w.t0, [&](int, bool) {
-                    issue();
-                    if (first) {
-                        first = false;
-                        if (!wait(q_empty, q_ph)) return false;
-                        q_ph ^= 1;
-                        const int qc = tid % kChunks, qr = tid / kChunks;
-                        for (int b = 0; b < MT; ++b)
+                const int n = w.t1 - w.t0;
+                if (!__all_sync(0xffffffffu, wait(q_empty, q_ph))) break;
+                q_ph ^= 1;
+                const int qc = tid % kChunks, qr = tid / kChunks;
 #pragma unroll 4
-                            for (int k = 0; k < kT * kChunks / 256; ++k) {
-                                const int r = qr + k * (256 / kChunks), row = b * kT + r;
-                                uint4 x = make_uint4(0, 0, 0, 0);
-                                if (row < rows)
-                                    x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                                        q_offset(p, w.e, w.h, row0 + row, D) + qc * 8);
-                                *reinterpret_cast<uint4*>(smem + b * kT * D * 2 + tile_at(r, qc)) = x;
-                            }
-                    }
-                    if (!wait(empty + ring.i, ring.ph ^ 1)) return false;
+                for (int k = 0; k < MT * kT * kChunks / 256; ++k) {
+                    const int row = qr + k * (256 / kChunks);
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (row < rows)
+                        x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                            q_offset(p, w.e, w.h, row0 + row, D) + qc * 8);
+                    *reinterpret_cast<uint4*>(smem + (row / kT) * kT * D * 2 + tile_at(row % kT, qc)) = x;
+                }
+                bool ok = true;
+                for (int k = 0; k < 2 * n; ++k) {
+                    issue();
+                    ok = __all_sync(0xffffffffu, wait(empty + ring.i, ring.ph ^ 1));
+                    if (!ok) break;
                     cp_async_wait<C::kRaw - 1>();
                     uint8_t* dst = smem + C::oStage + ring.i * C::kStage;
 #pragma unroll
-                    for (int k = 0; k < kMine; ++k) {
-                        const int r = r0 + k * kStep;
-                        const uint4 x = *reinterpret_cast<const uint4*>(raw + slot * C::kRawBytes + k * 4096);
-                        const uint2 a = widen4(x.x), b = widen4(x.y), d = widen4(x.z), f = widen4(x.w);
+                    for (int x = 0; x < kMine; ++x) {
+                        const int r = r0 + x * kStep;
+                        const uint4 y = *reinterpret_cast<const uint4*>(raw + slot * C::kRawBytes + x * 4096);
+                        const uint2 a = widen4(y.x), b = widen4(y.y), d = widen4(y.z), f = widen4(y.w);
                         *reinterpret_cast<uint4*>(dst + tile_at(r, 2 * c)) = make_uint4(a.x, a.y, b.x, b.y);
                         *reinterpret_cast<uint4*>(dst + tile_at(r, 2 * c + 1)) = make_uint4(d.x, d.y, f.x, f.y);
                     }
@@ -386,42 +426,53 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                     mbar_arrive(full + ring.i);
                     ring.next();
                     if (++slot == C::kRaw) slot = 0;
-                    return true;
-                });
+                }
+                if (!ok) break;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
-    } else if (warp == 8) {
+    } else if (warp >= 8) {
         // ----------------------------------------------------------- products
+        reg_dec<C::kRegMma>();
+        if (warp > 8) u = end;  // one warp issues; its group's others only gave registers back
         Ring<NS> ring;
         uint32_t p_ph[2] = {0, 0};
         constexpr uint32_t kS = instr_desc(kT, false), kO = instr_desc(D, true);
         const uint32_t q_addr = smem_u32(smem), st_addr = smem_u32(smem + C::oStage);
         auto s_of = [&](int s) { return tmem + s * kT; };
         auto o_of = [&](int s) { return tmem + 2 * kT + s * D; };
+        // The whole warp walks along, so addresses stay warp-uniform; one lane issues.
+        auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         auto ready = [&](const Ring<NS>& r) {
-            if (!wait(full + r.i, r.ph)) return false;
+            if (!all_wait(full + r.i, r.ph)) return false;
             proxy_fence();  // the copies' writes, before the products read them
             return true;
         };
+        auto commit = [&](uint64_t* bar) { if (elected()) tc_commit(bar); };
         auto scores = [&](int s, int stage) {  // S = Q K^T of stream s
-            const uint32_t a = q_addr + (MT == 2 ? s : 0) * kT * D * 2, b = st_addr + stage * C::kStage;
+            const uint32_t d = s_of(s);
+            const uint64_t a = smem_desc(q_addr + (MT == 2 ? s : 0) * kT * D * 2, 16, 1024);
+            const uint64_t b = smem_desc(st_addr + stage * C::kStage, 16, 1024);
+            if (elected()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * (kT * 128) + (k & 3) * 32;
-                mma_ss(s_of(s), smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), kS, k > 0);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * (kT * 128) + (k & 3) * 32) >> 4;
+                    mma_ss(d, a + off, b + off, kS, k > 0);
+                }
+                tc_commit(s_full + s);
             }
-            tc_commit(s_full + s);
         };
         auto values = [&](int s, int stage, bool add) {  // O += P V of stream s
-            const uint32_t b = st_addr + stage * C::kStage;
+            const uint32_t d = o_of(s), a = s_of(s);
+            const uint64_t b = smem_desc(st_addr + stage * C::kStage, kT * 128, 1024);
+            if (elected()) {
 #pragma unroll
-            for (int k = 0; k < kT / 16; ++k)
-                mma_ts(o_of(s), s_of(s) + k * 8, smem_desc(b + k * 2048, kT * 128, 1024), kO, add || k > 0);
-            tc_commit(o_done + s);
+                for (int k = 0; k < kT / 16; ++k) mma_ts(d, a + k * 8, b + k * 128, kO, add || k > 0);
+                tc_commit(o_done + s);
+            }
         };
         auto weights = [&](int s) {  // P of stream s is there
-            if (!wait(p_full + s, p_ph[s])) return false;
+            if (!all_wait(p_full + s, p_ph[s])) return false;
             p_ph[s] ^= 1;
             tc_fence_after();
             return true;
@@ -430,75 +481,62 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             if (w.nodes * p.G - w.mt * p.tile_rows <= 0) continue;
             const int n = w.t1 - w.t0;
             bool ok = true;
-            if (lane == 0) {
-                if (MT == 1) {
-                    for (int i = 0; ok && i < n && i < 2; ++i) {
+            if (MT == 1) {
+                // S of the first two tiles, then PV of tile i and S of tile i + 2
+                for (int i = -2; ok && i < n; ++i) {
+                    if (i >= 0) {
+                        ok = ready(ring) && weights(i & 1);
+                        if (!ok) break;
+                        values(i & 1, ring.i, i >= 2);
+                        commit(empty + ring.i);
+                        ring.next();
+                    }
+                    if (i + 2 < n) {
                         ok = ready(ring);
                         if (!ok) break;
-                        scores(i, ring.i);
-                        tc_commit(empty + ring.i);
-                        if (i + 1 == n) tc_commit(q_empty);
+                        scores(i & 1, ring.i);
+                        commit(empty + ring.i);
+                        if (i + 3 == n) commit(q_empty);
                         ring.next();
                     }
-                    for (int i = 0; ok && i < n; ++i) {
-                        const int s = i & 1;
-                        ok = ready(ring) && weights(s);
-                        if (!ok) break;
-                        values(s, ring.i, i >= 2);
-                        tc_commit(empty + ring.i);
-                        ring.next();
-                        if (i + 2 < n) {
-                            ok = ready(ring);
+                }
+            } else {
+                // of each stream: PV of tile i, then S of tile i + 1
+                Ring<NS> rv = ring;
+                for (int i = -1; ok && i < n; ++i) {
+                    const bool more = i + 1 < n;
+                    if (i >= 0) { rv = ring; ring.next(); }
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (i >= 0) {
+                            ok = (s > 0 || ready(rv)) && weights(s);
+                            if (!ok) break;
+                            values(s, rv.i, i > 0);
+                        }
+                        if (more) {
+                            ok = s > 0 || ready(ring);
                             if (!ok) break;
                             scores(s, ring.i);
-                            tc_commit(empty + ring.i);
-                            if (i + 3 == n) tc_commit(q_empty);
-                            ring.next();
                         }
                     }
-                } else {
-                    ok = ready(ring);
-                    if (ok) {
-                        scores(0, ring.i);
-                        scores(1, ring.i);
-                        tc_commit(empty + ring.i);
-                        if (n == 1) tc_commit(q_empty);
+                    if (!ok) break;
+                    if (i >= 0) commit(empty + rv.i);
+                    if (more) {
+                        commit(empty + ring.i);
+                        if (i + 2 == n) commit(q_empty);
                         ring.next();
                     }
-                    for (int i = 0; ok && i < n; ++i) {
-                        const Ring<NS> rv = ring;
-                        ring.next();
-                        const bool more = i + 1 < n;
-                        ok = ready(rv) && weights(0);
-                        if (!ok) break;
-                        values(0, rv.i, i > 0);
-                        if (more) {
-                            ok = ready(ring);
-                            if (!ok) break;
-                            scores(0, ring.i);
-                        }
-                        ok = weights(1);
-                        if (!ok) break;
-                        values(1, rv.i, i > 0);
-                        tc_commit(empty + rv.i);
-                        if (more) {
-                            scores(1, ring.i);
-                            tc_commit(empty + ring.i);
-                            if (i + 2 == n) tc_commit(q_empty);
-                            ring.next();
-                        }
-                    }
-                }
-                if (!ok) {  // products in flight end before the tensor memory is given back
-                    tc_commit(drain);
-                    mbar_wait_bounded(drain, 0, p.err, 3, 10000000ull);
                 }
             }
-            __syncwarp();
-            if (__shfl_sync(0xffffffffu, (int)ok, 0) == 0) break;
+            if (!ok) {  // products in flight end before the tensor memory is given back
+                commit(drain);
+                mbar_wait_bounded(drain, 0, p.err, 3, 10000000ull);
+                break;
+            }
         }
     } else {
         // ------------------------------------------------------------ softmax
+        reg_inc<C::kRegSoftmax>();
         // a wait that all lanes leave with the same answer
         auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         const int st = warp >> 2;                   // stream
@@ -521,28 +559,43 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             const int node = (row0 + item_row) / p.G;
             float m = -INFINITY, l = 0.f;
             int done = 0;  // tiles of this stream
-            for (int i = MT == 1 ? st : 0; i < n; i += MT == 1 ? 2 : 1) {
+            constexpr int kEvery = MT == 1 ? 2 : 1;  // token tiles from one of this stream's to its next
+            const int i0 = MT == 1 ? st : 0;
+            // scales of a tile's rows (8-bit): lane l has rows l, l + 32 ..; 0 past the sequence
+            float sc_k[kT / 32], sc_v[kT / 32];
+            auto scales = [&](int tok) {
+#pragma unroll
+                for (int k = 0; k < kT / 32; ++k) {
+                    const int t = tok + k * 32 + lane;
+                    const bool there = t < tokens;
+                    const long long row = there ? tree_row(p.at, w.e, w.h, t) : 0;
+                    sc_k[k] = there ? __ldg(p.k_scale + row) : 0.f;
+                    sc_v[k] = there ? __ldg(p.v_scale + row) : 0.f;
+                }
+            };
+            if (C::kQ8 && i0 < n) scales((w.t0 + i0) * kT);
+            for (int i = i0; i < n; i += kEvery) {
                 const int tok0 = (w.t0 + i) * kT;
                 const bool masked = tok0 + kT > w.prefix;
-                if constexpr (C::kQ8) {  // the tile's scales, ahead of S
+                if constexpr (C::kQ8) {  // the tile's scales; those of the stream's next tile are read meanwhile
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < kT / 32; ++k) {
-                        const int t = k * 32 + lane;
-                        float a = 0.f, b = 0.f;
-                        if (tok0 + t < tokens) {
-                            const long long row = tree_row(p.at, w.e, w.h, tok0 + t);
-                            a = __ldg(p.k_scale + row) * p.qscale;
-                            b = __ldg(p.v_scale + row);
+                        const int j = tok0 + k * 32 + lane - w.prefix;
+                        float a = sc_k[k] * p.qscale, b = sc_v[k];
+                        if (j >= 0 && !(isfinite(a) && isfinite(b))) {  // a tree row, not seen by all: set aside
+                            a = b = 0.f;
+                            atomicOr(bad + (j >> 5), 1u << (j & 31));
                         }
-                        ks[t] = a;
-                        vs[t] = b;
+                        ks[k * 32 + lane] = a;
+                        vs[k * 32 + lane] = b;
                     }
                     __syncwarp();
+                    if (i + kEvery < n) scales(tok0 + kEvery * kT);
                 }
                 if (masked) {
                     // values of tree rows that are not finite leave the stage (see the top)
-                    const long long use = uses + (MT == 2 ? 2 * i + 1 : n == 1 ? 1 : i < n - 1 ? 2 * i + 2 : 2 * i + 1);
+                    const long long use = uses + v_use<MT>(i, n);
                     const int stage = (int)(use % NS);
                     ok = all_wait(full + stage, (uint32_t)(use / NS) & 1);
                     if (!ok) break;
@@ -571,28 +624,50 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                 s_ph ^= 1;
                 tc_fence_after();
                 if (warp_live) {
-                    uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-                    if (masked) {
+                    if (masked) {  // what a row does not see gets the score -infinity
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t vis = live ? visible(p, w.e, node, w.nodes, tok0 + 32 * k - w.prefix) : 0u;
+                            uint32_t x[32];
+                            tc_ld32(x, t_s + 32 * k);
+                            tc_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            vis[k] = live ? visible(p, w.e, node, w.nodes, tok0 + 32 * k - w.prefix) : 0u;
+                            for (int j = 0; j < 32; ++j) {
+                                float f = __uint_as_float(x[j]);
+                                if constexpr (C::kQ8) f *= ks[32 * k + j];
+                                x[j] = (vis >> j & 1) ? __float_as_uint(f) : 0xff800000u;
+                            }
+                            tc_st32(t_s + 32 * k, x);
+                        }
+                        tc_wait_st();
+                        if constexpr (C::kQ8) {  // the scales are in these scores
+                            __syncwarp();
+                            for (int k = lane; k < kT; k += 32) ks[k] = 1.f;
+                            __syncwarp();
+                        }
                     }
                     // the tile's maximum
                     float mx = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t x[32];
-                        tc_ld32(x, t_s + 32 * k);
+#pragma unroll 1
+                    for (int k = 0; k < 4; k += 2) {
+                        uint32_t x[2][32];
+                        tc_ld32(x[0], t_s + 32 * k);
+                        tc_ld32(x[1], t_s + 32 * k + 32);
                         tc_wait_ld();
-                        float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        float a[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            float f = __uint_as_float(x[j]);
-                            if constexpr (C::kQ8) f *= ks[32 * k + j];
-                            if (masked) f = (vis[k] >> j & 1) ? f : -INFINITY;
-                            a[j & 3] = fmaxf(a[j & 3], f);
+                        for (int j = 0; j < 64; j += 4) {
+                            float f[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) f[q] = __uint_as_float(x[j >> 5][(j & 31) + q]);
+                            if constexpr (C::kQ8) {
+                                const float4 sc = *reinterpret_cast<const float4*>(ks + 32 * k + j);
+                                f[0] *= sc.x; f[1] *= sc.y; f[2] *= sc.z; f[3] *= sc.w;
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) a[q] = fmaxf(a[q], f[q]);
                         }
-                        mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
+                        mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                     }
                     if constexpr (!C::kQ8) mx *= p.qscale;
                     if (done == 0) {
@@ -620,27 +695,42 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                     }
                     const float base = m == -INFINITY ? 0.f : -m;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t x[32], y[16];
-                        tc_ld32(x, t_s + 32 * k);
+#pragma unroll 1
+                    for (int k = 0; k < 4; k += 2) {
+                        uint32_t x[2][32];
+                        tc_ld32(x[0], t_s + 32 * k);
+                        tc_ld32(x[1], t_s + 32 * k + 32);
                         tc_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float f = __uint_as_float(x[j]);
-                            float e = ex2(C::kQ8 ? fmaf(f, ks[32 * k + j], base) : fmaf(f, p.qscale, base));
-                            if (masked) e = (vis[k] >> j & 1) ? e : 0.f;
-                            sum[j & 3] += e;
-                            if constexpr (C::kQ8) {
-                                e *= vs[32 * k + j];
-                                if (masked) e = (vis[k] >> j & 1) ? e : 0.f;
-                            }
-                            x[j] = __float_as_uint(e);
-                        }
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t y[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            y[j] = pack_bf16x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
-                        tc_st16(t_s + 16 * k, y);
+                            for (int j = 0; j < 32; j += 4) {
+                                float f[4];
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) f[q] = __uint_as_float(x[h][j + q]);
+                                if constexpr (C::kQ8) {
+                                    const float4 sc = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j);
+                                    f[0] = fmaf(f[0], sc.x, base); f[1] = fmaf(f[1], sc.y, base);
+                                    f[2] = fmaf(f[2], sc.z, base); f[3] = fmaf(f[3], sc.w, base);
+                                } else {
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) f[q] = fmaf(f[q], p.qscale, base);
+                                }
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    f[q] = ex2(f[q]);
+                                    sum[q] += f[q];
+                                }
+                                if constexpr (C::kQ8) {
+                                    const float4 sc = *reinterpret_cast<const float4*>(vs + 32 * (k + h) + j);
+                                    f[0] *= sc.x; f[1] *= sc.y; f[2] *= sc.z; f[3] *= sc.w;
+                                }
+                                y[j / 2] = pack_bf16x2(f[0], f[1]);
+                                y[j / 2 + 1] = pack_bf16x2(f[2], f[3]);
+                            }
+                            tc_st16(t_s + 16 * (k + h), y);
+                        }
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tc_wait_st();
@@ -711,12 +801,15 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                             uint32_t see = bad[q] & mask_word(p, w.e, node, q);
                             for (; see; see &= see - 1) {
                                 const long long row = tree_row(p.at, w.e, w.h, w.prefix + 32 * q + __ffs(see) - 1);
+                                bool fine = true;
+                                if constexpr (C::kQ8)
+                                    fine = isfinite(p.k_scale[row] * p.qscale) && isfinite(p.v_scale[row]);
 #pragma unroll
                                 for (int j = 0; j < 32; ++j) {
                                     float f;
-                                    if constexpr (C::kQ8) {
+                                    if constexpr (C::kQ8) {  // NaN in a channel, or throughout by its row's scales
                                         const uint8_t code = static_cast<const uint8_t*>(p.v)[row * D + col + j];
-                                        f = (code & 0x7f) == 0x7f ? NAN : 0.f;
+                                        f = (code & 0x7f) == 0x7f || !fine ? NAN : 0.f;
                                     } else {
                                         f = Elem<bf16_t>::to_f32(static_cast<const bf16_t*>(p.v)[row * D + col + j]);
                                         f = isfinite(f) ? 0.f : f;
