@@ -25,6 +25,7 @@ struct TreeParams {
     const int32_t *mask, *seq_lens, *node_lens;
     CacheRows at;
     int b, t, hq, hkv, G, s;
+    long long cache_rows;  // rows of the whole cache or pool
     int rows;        // t * G
     int tile_rows;   // rows of a row tile
     int n_mt;        // row tiles of a (entry, kv head)
@@ -216,7 +217,6 @@ cudaError_t launch_tree_simt(const TreeParams& p, int d, cudaStream_t st);
 // bf16 and e4m3 (ds_tree_tc.cu; up to 64 query rows: ds_tree_few.cu).
 TreePlan plan_tree_tc(int rows, int d);
 cudaError_t launch_tree_tc(const TreeParams& p, int type, int d, cudaStream_t st);
-cudaError_t launch_tree_few(const TreeParams& p, int type, int d, cudaStream_t st);
 cudaError_t launch_tree_combine(const TreeParams& p, int d, cudaStream_t st);
 
 }  // namespace ds

@@ -186,6 +186,8 @@ ds_status tree_decode(const void* q, const void* k, const void* v, ds_dtype kvdt
     p.mask = mask; p.seq_lens = seq_lens; p.node_lens = node_lens;
     p.b = b; p.t = t; p.hq = hq; p.hkv = hkv; p.G = hq / hkv; p.s = s;
     p.rows = t * p.G;
+    p.cache_rows = pool ? (long long)pool->num_blocks * hkv << p.at.page_shift : (long long)b * hkv * s_cap;
+    if (p.cache_rows > 0x7fffffffll - 256) DS_FAIL(DS_ERR_UNSUPPORTED, "a cache of 2^31 rows");
     p.tile_rows = sh.plan.tile_rows; p.tile_tokens = sh.plan.tile_tokens;
     p.n_mt = sh.n_mt; p.part_rows = sh.part_rows; p.grid = sh.grid;
     p.qscale = (sm_scale > 0.f ? sm_scale : 1.0f / sqrtf((float)d)) * 1.4426950408889634f;

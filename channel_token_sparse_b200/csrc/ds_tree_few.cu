@@ -27,21 +27,19 @@ constexpr float kFloor = -3.0e38f;  // a maximum before any token
 template <int TYPE, int D, int N>
 struct Cfg {
     static constexpr bool kQ8 = TYPE == kTreeE4M3;
-    static constexpr int kLoadWarps = kQ8 ? 8 : 4;
-    static constexpr int kThreads = (12 + kLoadWarps) * 32;
-    // As in ds_tree_tc.cu: 168 + 168 + 88 + 88 = 4 * 128; 8-bit: 104 + 104 + 64
-    // + 2 * 104 (N = 32: 120 and 88, N = 64: 136 and 72) = 5 * 96.
-    static constexpr int kRegSoftmax = kQ8 ? (N == 64 ? 136 : N == 32 ? 120 : 104) : 168, kRegMma = kQ8 ? 64 : 88;
-    static constexpr int kRegLoad = kQ8 ? (N == 64 ? 72 : N == 32 ? 88 : 104) : 88;
-    static constexpr int kDepth = N >= 32 ? 2 : 3;  // 8-bit tiles a loader has in registers
-    static_assert(2 * kRegSoftmax + kRegMma + (kQ8 ? 2 : 1) * kRegLoad <= (kQ8 ? 5 * 96 : 4 * 128), "registers");
+    static constexpr int kThreads = kQ8 ? 640 : 384;
+    // Registers of a thread by role (see ds_tree_tc.cu): launched with 168
+    // (8-bit: 96), 208 + 208 + 88 = 3 * 168 and 152 + 152 + 64 + 2 * 56 = 5 * 96.
+    static constexpr int kRegSoftmax = kQ8 ? 152 : 208, kRegMma = kQ8 ? 64 : 88, kRegWiden = 56;
+    static_assert(kQ8 ? 2 * kRegSoftmax + kRegMma + 2 * kRegWiden <= 5 * 96 : 2 * kRegSoftmax + kRegMma <= 3 * 168, "");
     static constexpr int kStage = kT * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kStages = D == 128 ? (kQ8 ? 3 : 5) : (kQ8 ? 6 : 10);
+    static constexpr int kRaw = kQ8 ? 4 : 0, kRawBytes = kT * 128;  // slots of 8-bit tiles
     static constexpr int kQ = N * D * 2, kP = kT * 128;  // P^T: a token's weights in 128 bytes
-    static constexpr int oP = kQ, oStage = oP + 2 * kP, oStat = oStage + kStages * kStage;
+    static constexpr int oP = kQ, oStage = oP + 2 * kP, oRaw = oStage + kStages * kStage, oStat = oRaw + kRaw * kRawBytes;
     static constexpr int kStat = 16 * N;  // floats: maxima [2][N], factors [2][N], partial [2][4][N], result [4][N]
     static constexpr int oBar = oStat + kStat * 4;
-    static constexpr int kBars = 2 * kStages + 11;
+    static constexpr int kBars = 2 * kStages + 2 * kRaw + 12;
     static constexpr int kSmem = oBar + kBars * 8 + 64;
     static_assert(kSmem <= 227 * 1024 && kQ % 1024 == 0, "shared memory");
     static constexpr int kCols = N == 64 ? 512 : N == 32 ? 256 : 128;  // tensor memory: 4 S^T, 2 O^T of N columns
@@ -89,7 +87,8 @@ template <int V, bool MAX> __device__ __forceinline__ float warp_reduce_to_lane(
 }
 
 template <int TYPE, int D, int N>
-__global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kernel(
+    const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
     using C = Cfg<TYPE, D, N>;
     constexpr int NS = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -103,9 +102,12 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
     uint64_t* p_full = s_full + 4;   // [2] its P^T is, and O^T is ready to take it
     uint64_t* o_done = p_full + 2;   // [2] O^T has taken it
     uint64_t* q_empty = o_done + 2;  // the piece's S^T products are done
-    uint64_t* xch = q_empty + 1;     // softmax warps among themselves
+    uint64_t* q_full = q_empty + 1;  // its queries are there
+    uint64_t* xch = q_full + 1;      // softmax warps among themselves
     uint64_t* drain = xch + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* raw_full = drain + 1;  // [kRaw] 8-bit tiles
+    uint64_t* raw_empty = raw_full + C::kRaw;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + C::kRaw);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
     uint32_t* bad = tmem_slot + 2;   // [8] nodes whose V row holds values that are not finite
 
@@ -113,8 +115,12 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, C::kLoadWarps * 32);
+            mbar_init(full + i, C::kQ8 ? 256 : 1);
             mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < C::kRaw; ++i) {
+            mbar_init(raw_full + i, 1);
+            mbar_init(raw_empty + i, 256);
         }
         for (int s = 0; s < 4; ++s) mbar_init(s_full + s, 1);
         for (int s = 0; s < 2; ++s) {
@@ -122,6 +128,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
             mbar_init(o_done + s, 1);
         }
         mbar_init(q_empty, 1);
+        mbar_init(q_full, 64);
         mbar_init(xch, 256);
         mbar_init(drain, 1);
         *stop = 0;
@@ -148,35 +155,39 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
     TreePiece w;
 
     if (warp >= 12) {
-        // ------------------------------------------------------------ loaders
-        reg_dec_or_inc<C::kRegLoad, (C::kQ8 ? 96 : 128)>();
-        const TcRing m{smem, smem + C::oStage, full, empty, q_empty};
-        const int tid = threadIdx.x - 12 * 32;
-        if constexpr (!C::kQ8) load_bf16<D, NS, N, FewOrder>(p, m, wait, cur, u, end, tid);
-        else load_e4m3<D, NS, N, FewOrder, C::kDepth>(p, m, wait, cur, u, end, tid);
+        // --------------------------------------------------- widening (8-bit)
+        if constexpr (C::kQ8) {
+            reg_dec<C::kRegWiden>();
+            widen_tiles<D, C::kRaw, NS>(p, smem + C::oRaw, raw_full, raw_empty, smem + C::oStage, full, empty, wait, cur, u,
+                                        end, threadIdx.x - 12 * 32);
+        }
     } else if (warp >= 8) {
-        // ----------------------------------------------------------- products
+        // -------------------------------------------------- copies, products
         reg_dec<C::kRegMma>();
-        if (warp > 8) u = end;  // one warp issues; its group's others only gave registers back
+        if (warp == 9) {
+            if constexpr (C::kQ8)
+                copy_tiles<TYPE, D, C::kRaw, FewOrder>(p, &maps.k, &maps.v, smem + C::oRaw, raw_full, raw_empty, wait, cur, u, end);
+            else
+                copy_tiles<TYPE, D, NS, FewOrder>(p, &maps.k, &maps.v, smem + C::oStage, full, empty, wait, cur, u, end);
+        } else if (warp >= 10) {
+            copy_queries<D, N>(p, smem, q_full, q_empty, wait, cur, u, end, threadIdx.x - 10 * 32);
+        }
+        if (warp > 8) u = end;  // the products are warp 8's
         Ring<NS> ring;
-        uint32_t p_ph[2] = {0, 0};
+        uint32_t p_ph[2] = {0, 0}, q_ph = 0;
         constexpr uint32_t kS = instr_desc(N, false, false), kO = instr_desc(N, true, true);
         const uint32_t q_addr = smem_u32(smem), p_addr = smem_u32(smem + C::oP), st_addr = smem_u32(smem + C::oStage);
-        auto ready = [&]() {
-            if (!all_wait(full + ring.i, ring.ph)) return false;
-            proxy_fence();  // the copies' writes, before the products read them
-            return true;
-        };
         auto commit = [&](uint64_t* bar) { if (elected()) tc_commit(bar); };
         while (next_piece(p, cur, u, end, w)) {
             if (w.nodes * p.G - w.mt * p.tile_rows <= 0) continue;
             const int n = w.t1 - w.t0;
-            bool ok = true;
+            bool ok = all_wait(q_full, q_ph);
+            q_ph ^= 1;
             // S^T of tile i + 2, then PV of tile i
-            for (int i = -2; i < n; ++i) {
+            for (int i = -2; ok && i < n; ++i) {
                 const int s = i & 1;
                 if (i + 2 < n) {
-                    ok = ready();
+                    ok = all_wait(full + ring.i, ring.ph);
                     if (!ok) break;
                     const int b = 2 * s + (((i + 2) >> 1) & 1);
                     const uint32_t d = tmem + b * N;
@@ -193,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                     ring.next();
                 }
                 if (i >= 0) {
-                    ok = ready() && all_wait(p_full + s, p_ph[s]);
+                    ok = all_wait(full + ring.i, ring.ph) && all_wait(p_full + s, p_ph[s]);
                     if (!ok) break;
                     p_ph[s] ^= 1;
                     tc_fence_after();
@@ -258,7 +269,6 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                         ks = vs = 0.f;
                         atomicOr(bad + (node_t >> 5), 1u << (node_t & 31));
                     }
-                    if (i + 2 < n) scales(tok0 + 2 * kT + t);
                 }
                 bool fine = true;
                 unsigned long long vis = ~0ull;  // query rows that see this token
@@ -270,12 +280,14 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                         for (int r = 0, x = row0 / p.G; r < rows; ++x, r += p.G)
                             if (mask_word(p, w.e, x, node_t >> 5) >> (node_t & 31) & 1) vis |= g << r;
                     }
-                    // values of tree rows that are not finite leave the stage (see ds_tree_tc.cu)
+                }
+                if (masked && !C::kQ8) {
+                    // the stage is tidied first (see ds_tree_tc.cu)
                     const unsigned use = uses + FewOrder::v_use(i, n), stage = use % NS;
                     fine = all_wait(full + stage, use / NS & 1);
-                    const int b = max(w.prefix - tok0, 0), cnt = fine ? min(tokens - tok0, kT) - b : 0;
-                    if (clear_not_finite<D>(smem + C::oStage + stage * C::kStage, b, cnt, tok0 - w.prefix, bad, t))
-                        proxy_fence();
+                    if (fine)
+                        tidy_values<D>(smem + C::oStage + stage * C::kStage, max(w.prefix - tok0, 0),
+                                       min(tokens - tok0, kT), tok0 - w.prefix, bad, t);
                 }
                 const int buf = (i >> 1) & 1;
                 fine = all_wait(s_full + 2 * st + buf, s_ph[buf]) && fine;
@@ -367,6 +379,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                 proxy_fence();
                 tc_fence_before();
                 mbar_arrive(p_full + st);
+                if (C::kQ8 && i + 2 < n) scales(tok0 + 2 * kT + t);  // (before, the fence would wait for them)
                 ++o_cnt;
                 ++done;
             }
@@ -475,20 +488,20 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
 }
 
 template <int TYPE, int D, int N>
-cudaError_t run(const TreeParams& p, cudaStream_t st) {
+cudaError_t run(const TreeParams& p, const TreeMaps& m, cudaStream_t st) {
     using C = Cfg<TYPE, D, N>;
     cudaError_t e = cudaFuncSetAttribute(ds_tree_few_kernel<TYPE, D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kSmem);
     if (e != cudaSuccess) return e;
-    ds_tree_few_kernel<TYPE, D, N><<<p.grid, C::kThreads, C::kSmem, st>>>(p);
+    ds_tree_few_kernel<TYPE, D, N><<<p.grid, C::kThreads, C::kSmem, st>>>(p, m);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree_few(const TreeParams& p, int type, int d, cudaStream_t st) {
+cudaError_t launch_tree_few(const TreeParams& p, const TreeMaps& m, int type, int d, cudaStream_t st) {
 #define DS_N(TY, D_) \
-    (p.tile_rows == 16 ? run<TY, D_, 16>(p, st) : p.tile_rows == 32 ? run<TY, D_, 32>(p, st) : run<TY, D_, 64>(p, st))
+    (p.tile_rows == 16 ? run<TY, D_, 16>(p, m, st) : p.tile_rows == 32 ? run<TY, D_, 32>(p, m, st) : run<TY, D_, 64>(p, m, st))
     if (type == kTreeBF16) return d == 64 ? DS_N(kTreeBF16, 64) : DS_N(kTreeBF16, 128);
     return d == 64 ? DS_N(kTreeE4M3, 64) : DS_N(kTreeE4M3, 128);
 #undef DS_N

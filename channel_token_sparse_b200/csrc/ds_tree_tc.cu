@@ -14,14 +14,15 @@
 // and both use every token tile, which halves the reads a row costs.
 //
 // Roles: warps 0-3 and 4-7 softmax of stream 0 and 1 (a thread a row), warp 8
-// issues the products, warps 12 on bring K and V tiles into a ring of
-// 128-byte-swizzled stages (any page size; rows past the sequence become
-// zeros): bf16 by 16-byte asynchronous copies, 8-bit codes through registers,
-// where they are widened to bf16 (exact); their rows' scales multiply S and P.
+// issues the products, warp 9 brings K and V tiles into a ring of
+// 128-byte-swizzled stages by tensor copies (any page size), warps 10 and 11
+// the queries. 8-bit tiles land in slots of their own and warps 12 to 19 widen
+// them to bf16 (exact) into the ring; their rows' scales multiply S and P.
 //
 // The products take every row of V with every weight, and 0 * NaN is NaN, so
-// the rows of tree nodes (which some query rows may not see) are looked
-// through for values that are not finite; such values are zeroed in the stage
+// the softmax warps tidy a tile that reaches past the prefix: rows past the
+// sequence become zeros, and the rows of tree nodes (which some query rows may
+// not see) are looked through for values that are not finite, which are zeroed
 // and added to the rows that do see them at the end. An 8-bit tree row whose
 // scales are not finite is set aside the same way.
 #include "ds_tree_tc.cuh"
@@ -33,21 +34,21 @@ namespace {
 template <int TYPE, int D, int MT>
 struct Cfg {
     static constexpr bool kQ8 = TYPE == kTreeE4M3;
-    static constexpr int kLoadWarps = kQ8 ? 8 : 4;
-    static constexpr int kThreads = (12 + kLoadWarps) * 32;
-    // Registers of a thread by role: 512 (8-bit: 640) threads are launched with
-    // 128 (96) each, and the four-warp groups redistribute them: their sums are
-    // 168 + 168 + 72 + 104 = 4 * 128 and 128 + 128 + 64 + 2 * 80 = 5 * 96.
-    static constexpr int kRegSoftmax = kQ8 ? 128 : 168, kRegMma = kQ8 ? 64 : 72, kRegLoad = kQ8 ? 80 : 104;
-    static_assert(2 * kRegSoftmax + kRegMma + (kQ8 ? 2 : 1) * kRegLoad <= (kQ8 ? 5 * 96 : 4 * 128), "registers");
+    static constexpr int kThreads = kQ8 ? 640 : 384;
+    // Registers of a thread by role: 384 (8-bit: 640) threads are launched with
+    // 168 (96) each, and the four-warp groups redistribute them: their sums are
+    // 208 + 208 + 88 = 3 * 168 and 152 + 152 + 64 + 2 * 56 = 5 * 96.
+    static constexpr int kRegSoftmax = kQ8 ? 152 : 208, kRegMma = kQ8 ? 64 : 88, kRegWiden = 56;
+    static_assert(kQ8 ? 2 * kRegSoftmax + kRegMma + 2 * kRegWiden <= 5 * 96 : 2 * kRegSoftmax + kRegMma <= 3 * 168, "");
     static constexpr int kStage = kT * D * 2;       // bytes of a K or V tile in bf16
     static constexpr int kQ = MT * kT * D * 2;
+    static constexpr int kRaw = kQ8 ? 3 : 0, kRawBytes = kT * 128;  // slots of 8-bit tiles
     static constexpr int kScale = kQ8 ? 8 * 2 * kT * 4 : 0;  // a softmax warp's K and V scales of a tile
-    static constexpr int kStages = D == 128 ? 7 - MT - kQ8 : 13 - MT;
-    static constexpr int oStage = kQ, oScale = oStage + kStages * kStage;
+    static constexpr int kStages = D == 128 ? 7 - MT - 2 * kQ8 : 13 - MT - 4 * kQ8;
+    static constexpr int oStage = kQ, oRaw = oStage + kStages * kStage, oScale = oRaw + kRaw * kRawBytes;
     static constexpr int oMl = oScale + kScale;             // [2][128] maxima, [2][128] sums
     static constexpr int oBar = oMl + 4 * kT * 4;
-    static constexpr int kBars = 2 * kStages + 9;
+    static constexpr int kBars = 2 * kStages + 2 * kRaw + 10;
     static constexpr int kSmem = oBar + kBars * 8 + 64;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -70,7 +71,8 @@ template <int MT> struct TcOrder {
 // -------------------------------------------------------------------- kernel
 
 template <int TYPE, int D, int MT>
-__global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kernel(
+    const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
     using C = Cfg<TYPE, D, MT>;
     constexpr int NS = C::kStages;
         extern __shared__ __align__(1024) uint8_t smem[];
@@ -81,9 +83,12 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
     uint64_t* p_full = s_full + 2;   // [2] its P is, and O is ready to take it
     uint64_t* o_done = p_full + 2;   // [2] O has taken it
     uint64_t* q_empty = o_done + 2;  // the piece's S products are done
-    uint64_t* xch = q_empty + 1;     // softmax warps among themselves
+    uint64_t* q_full = q_empty + 1;  // its queries are there
+    uint64_t* xch = q_full + 1;      // softmax warps among themselves
     uint64_t* drain = xch + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* raw_full = drain + 1;  // [kRaw] 8-bit tiles
+    uint64_t* raw_empty = raw_full + C::kRaw;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + C::kRaw);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
     uint32_t* bad = tmem_slot + 2;   // [8] nodes whose V row holds values that are not finite
 
@@ -91,8 +96,12 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, C::kLoadWarps * 32);
+            mbar_init(full + i, C::kQ8 ? 256 : 1);
             mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < C::kRaw; ++i) {
+            mbar_init(raw_full + i, 1);
+            mbar_init(raw_empty + i, 256);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + s, 1);
@@ -100,6 +109,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             mbar_init(o_done + s, 1);
         }
         mbar_init(q_empty, 1);
+        mbar_init(q_full, 64);
         mbar_init(xch, 256);
         mbar_init(drain, 1);
         *stop = 0;
@@ -125,29 +135,33 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
     TreePiece w;
 
     if (warp >= 12) {
-        // ------------------------------------------------------------ loaders
-        reg_dec<C::kRegLoad>();
-        const TcRing m{smem, smem + C::oStage, full, empty, q_empty};
-        const int tid = threadIdx.x - 12 * 32;
-        if constexpr (!C::kQ8) load_bf16<D, NS, MT * kT, TcOrder<MT>>(p, m, wait, cur, u, end, tid);
-        else load_e4m3<D, NS, MT * kT, TcOrder<MT>, 2>(p, m, wait, cur, u, end, tid);
+        // --------------------------------------------------- widening (8-bit)
+        if constexpr (C::kQ8) {
+            reg_dec<C::kRegWiden>();
+            widen_tiles<D, C::kRaw, NS>(p, smem + C::oRaw, raw_full, raw_empty, smem + C::oStage, full, empty, wait, cur, u,
+                                        end, threadIdx.x - 12 * 32);
+        }
     } else if (warp >= 8) {
-        // ----------------------------------------------------------- products
+        // -------------------------------------------------- copies, products
         reg_dec<C::kRegMma>();
-        if (warp > 8) u = end;  // one warp issues; its group's others only gave registers back
+        if (warp == 9) {
+            if constexpr (C::kQ8)
+                copy_tiles<TYPE, D, C::kRaw, TcOrder<MT>>(p, &maps.k, &maps.v, smem + C::oRaw, raw_full, raw_empty, wait, cur, u, end);
+            else
+                copy_tiles<TYPE, D, NS, TcOrder<MT>>(p, &maps.k, &maps.v, smem + C::oStage, full, empty, wait, cur, u, end);
+        } else if (warp >= 10) {
+            copy_queries<D, MT * kT>(p, smem, q_full, q_empty, wait, cur, u, end, threadIdx.x - 10 * 32);
+        }
+        if (warp > 8) u = end;  // the products are warp 8's
         Ring<NS> ring;
-        uint32_t p_ph[2] = {0, 0};
+        uint32_t p_ph[2] = {0, 0}, q_ph = 0;
         constexpr uint32_t kS = instr_desc(kT, false, false), kO = instr_desc(D, false, true);
         const uint32_t q_addr = smem_u32(smem), st_addr = smem_u32(smem + C::oStage);
         auto s_of = [&](int s) { return tmem + s * kT; };
         auto o_of = [&](int s) { return tmem + 2 * kT + s * D; };
         // The whole warp walks along, so addresses stay warp-uniform; one lane issues.
         auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-        auto ready = [&](const Ring<NS>& r) {
-            if (!all_wait(full + r.i, r.ph)) return false;
-            proxy_fence();  // the copies' writes, before the products read them
-            return true;
-        };
+        auto ready = [&](const Ring<NS>& r) { return all_wait(full + r.i, r.ph); };
         auto commit = [&](uint64_t* bar) { if (elected()) tc_commit(bar); };
         auto scores = [&](int s, int stage) {  // S = Q K^T of stream s
             const uint32_t d = s_of(s);
@@ -180,7 +194,8 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
         while (next_piece(p, cur, u, end, w)) {
             if (w.nodes * p.G - w.mt * p.tile_rows <= 0) continue;
             const int n = w.t1 - w.t0;
-            bool ok = true;
+            bool ok = all_wait(q_full, q_ph);
+            q_ph ^= 1;
             if (MT == 1) {
                 // S of the first two tiles, then PV of tile i and S of tile i + 2
                 for (int i = -2; ok && i < n; ++i) {
@@ -291,17 +306,15 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                         vs[k * 32 + lane] = b;
                     }
                     __syncwarp();
-                    if (i + kEvery < n) scales(tok0 + kEvery * kT);
                 }
-                if (masked) {
-                    // values of tree rows that are not finite leave the stage (see the top)
+                if (masked && !C::kQ8) {
+                    // the stage is tidied before the products read it (see the top)
                     const unsigned use = uses + TcOrder<MT>::v_use(i, n), stage = use % NS;
                     ok = all_wait(full + stage, use / NS & 1);
                     if (!ok) break;
-                    const int b = max(w.prefix - tok0, 0), cnt = min(tokens - tok0, kT) - b;
-                    if (clear_not_finite<D>(smem + C::oStage + stage * C::kStage, b, cnt, tok0 - w.prefix, bad,
-                                            threadIdx.x & 127))
-                        proxy_fence();
+                    tidy_values<D>(smem + C::oStage + stage * C::kStage, max(w.prefix - tok0, 0), min(tokens - tok0, kT),
+                                   tok0 - w.prefix, bad, threadIdx.x & 127);
+                    proxy_fence();
                 }
                 ok = all_wait(s_full + st, s_ph);
                 if (!ok) break;
@@ -421,6 +434,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                 }
                 tc_fence_before();
                 mbar_arrive(p_full + st);
+                if (C::kQ8 && i + kEvery < n) scales(tok0 + kEvery * kT);
                 ++o_cnt;
                 ++done;
             }
@@ -529,16 +543,45 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
 }
 
 template <int TYPE, int D, int MT>
-cudaError_t run(const TreeParams& p, cudaStream_t st) {
+cudaError_t run(const TreeParams& p, const TreeMaps& m, cudaStream_t st) {
     using C = Cfg<TYPE, D, MT>;
     cudaError_t e = cudaFuncSetAttribute(ds_tree_tc_kernel<TYPE, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::kSmem);
     if (e != cudaSuccess) return e;
-    ds_tree_tc_kernel<TYPE, D, MT><<<p.grid, C::kThreads, C::kSmem, st>>>(p);
+    ds_tree_tc_kernel<TYPE, D, MT><<<p.grid, C::kThreads, C::kSmem, st>>>(p, m);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+// The driver's encoder, fetched through the runtime (the library does not link
+// the driver library).
+cudaError_t make_tree_maps(const TreeParams& p, int type, int d, TreeMaps* m) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return cudaErrorNotSupported;
+    const bool q8 = type == kTreeE4M3;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)p.cache_rows}, stride[1] = {(cuuint64_t)(q8 ? d : 2 * d)};
+    const int page = p.at.block_table ? 1 << p.at.page_shift : kT;
+    const cuuint32_t box[2] = {(cuuint32_t)(q8 ? 128 : 64), (cuuint32_t)(page < kT ? page : kT)}, one[2] = {1, 1};
+    for (int i = 0; i < 2; ++i) {
+        const CUresult r = encode(i ? &m->v : &m->k, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                                  const_cast<void*>(i ? p.v : p.k), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    }
+    return cudaSuccess;
+}
 
 TreePlan plan_tree_tc(int rows, int d) {
     (void)d;
@@ -546,10 +589,15 @@ TreePlan plan_tree_tc(int rows, int d) {
     return TreePlan{tile, kT, 148};
 }
 
+cudaError_t launch_tree_few(const TreeParams& p, const TreeMaps& m, int type, int d, cudaStream_t st);
+
 cudaError_t launch_tree_tc(const TreeParams& p, int type, int d, cudaStream_t st) {
-    if (p.tile_rows < kT) return launch_tree_few(p, type, d, st);
+    TreeMaps m;
+    const cudaError_t e = make_tree_maps(p, type, d, &m);
+    if (e != cudaSuccess) return e;
+    if (p.tile_rows < kT) return launch_tree_few(p, m, type, d, st);
     const bool two = p.tile_rows == 2 * kT;
-#define DS_T(TY, D_) (two ? run<TY, D_, 2>(p, st) : run<TY, D_, 1>(p, st))
+#define DS_T(TY, D_) (two ? run<TY, D_, 2>(p, m, st) : run<TY, D_, 1>(p, m, st))
     if (type == kTreeBF16) return d == 64 ? DS_T(kTreeBF16, 64) : DS_T(kTreeBF16, 128);
     return d == 64 ? DS_T(kTreeE4M3, 64) : DS_T(kTreeE4M3, 128);
 #undef DS_T

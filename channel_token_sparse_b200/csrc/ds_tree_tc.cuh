@@ -2,6 +2,7 @@
 // tcgen05 wrappers, bounded waits, the ring of K and V stages and its loaders.
 #pragma once
 
+#include <cuda.h>
 #include <math.h>
 
 #include "ds_tree.cuh"
@@ -98,11 +99,6 @@ __device__ __forceinline__ bool elected() {
 }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-// To N registers from the FROM that the kernel was launched with.
-template <int N, int FROM> __device__ __forceinline__ void reg_dec_or_inc() {
-    if constexpr (N < FROM) reg_dec<N>();
-    else if constexpr (N > FROM) reg_inc<N>();
-}
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -139,11 +135,6 @@ template <int N> struct Ring {
     uint32_t ph = 0;
     __device__ __forceinline__ void next() { if (++i == N) { i = 0; ph ^= 1; } }
 };
-
-// 16 bytes from global to shared memory, or 16 zero bytes (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0));
-}
 
 // Byte offset of 16-byte chunk c (eight channels) of row r in a tile: blocks
 // of 64 channels of all `rows` rows, 128 bytes a row, chunks exchanged within
@@ -182,25 +173,6 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
     return make_uint2(widen2(__byte_perm(w, 0, 0x1404)), widen2(__byte_perm(w, 0, 0x3424)));
 }
 
-// The pages of a token tile: a lane keeps the block of the tile's rows 4 lane
-// .. 4 lane + 3, so one table read a warp and tile serves its 128 rows. Pages
-// of one or two rows are looked up row by row.
-struct TilePages {
-    int blk = 0;
-    __device__ __forceinline__ void load(const CacheRows& c, int e, int tok0, int tokens) {
-        if (c.page_shift < 2) return;
-        const int t = min(tok0 + 4 * lane_id(), tokens - 1);
-        blk = __ldg(c.block_table + (size_t)e * c.max_blocks + (t >> c.page_shift));
-        blk = min(max(blk, 0), c.num_blocks - 1);
-    }
-    // Pool row of token t = tok0 + r < tokens (called by whole warps).
-    __device__ __forceinline__ long long row(const CacheRows& c, int e, int h, int t, int r) const {
-        if (c.page_shift < 2) return tree_row(c, e, h, t);
-        const int b = __shfl_sync(0xffffffffu, blk, r >> 2);
-        return (((long long)b * c.hkv + h) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
-    }
-};
-
 // V columns of fp32 values, waited for.
 template <int V> __device__ __forceinline__ void load_columns(float (&x)[V], uint32_t addr) {
     uint32_t y[V];
@@ -216,28 +188,31 @@ template <int V> __device__ __forceinline__ void store_columns(uint32_t addr, co
     tc_st(addr, y);
 }
 
-// Zeroes the values that are not finite in rows [b, b + cnt) of a V stage (the
-// tile's tree rows; row 0 is node `node0`, negative in the prefix) and marks
-// their nodes; thread t of 128. True where this thread changed something.
+// Tidies rows [b, 128) of a bf16 V stage before the products read it: zeroes
+// the values that are not finite in the tile's tree rows [b, have) and marks
+// their nodes (row 0 is node `node0`, negative in the prefix), and clears the
+// rows past the sequence. Thread t of 128.
 template <int D>
-__device__ __forceinline__ bool clear_not_finite(uint8_t* v, int b, int cnt, int node0, uint32_t* bad, int t) {
+__device__ __forceinline__ void tidy_values(uint8_t* v, int b, int have, int node0, uint32_t* bad, int t) {
     constexpr int kChunks = D / 8;
-    bool changed = false;
-    for (int x = t; x < cnt * kChunks; x += 128) {
-        const int r = b + x / kChunks;
-        uint32_t* at = reinterpret_cast<uint32_t*>(v + tile_at(r, x % kChunks));
+    for (int x = b * kChunks + t; x < kT * kChunks; x += 128) {
+        const int r = x / kChunks;
+        uint4* at = reinterpret_cast<uint4*>(v + tile_at(r, x % kChunks));
+        if (r >= have) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        uint32_t* y = reinterpret_cast<uint32_t*>(at);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t y = at[k];
-            const bool lo = (y & 0x7f80u) == 0x7f80u, hi = (y & 0x7f800000u) == 0x7f800000u;
+            const uint32_t z = y[k];
+            const bool lo = (z & 0x7f80u) == 0x7f80u, hi = (z & 0x7f800000u) == 0x7f800000u;
             if (lo || hi) {
-                at[k] = y & (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+                y[k] = z & (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
                 atomicOr(bad + ((node0 + r) >> 5), 1u << ((node0 + r) & 31));
-                changed = true;
             }
         }
     }
-    return changed;
 }
 // What the marked nodes that `node` sees add to channel c: the sum of their
 // values that are not finite (8-bit: NaN, for a row whose scales are not).
@@ -271,158 +246,146 @@ __device__ __forceinline__ void add_result(const TreeParams& p, float* part, siz
     }
 }
 
-// What a CTA's roles share of its shared memory.
-struct TcRing {
-    uint8_t *q, *stages;             // queries; K and V tiles
-    uint64_t *full, *empty, *q_empty;
-};
-
-// The queries of a piece: QR rows (in blocks of at most 128), zeros past its own.
-template <int D, int QR, int THREADS>
-__device__ __forceinline__ void load_queries(const TreeParams& p, const TreePiece& w, uint8_t* q, int tid, bool async) {
-    constexpr int kChunks = D / 8, kB = QR < kT ? QR : kT;
-    const int row0 = w.mt * p.tile_rows, rows = w.nodes * p.G - row0;
-#pragma unroll 2
-    for (int x = tid; x < QR * kChunks; x += THREADS) {
-        const int row = x / kChunks, c = x % kChunks;
-        const bool there = row < rows;
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (there ? q_offset(p, w.e, w.h, row0 + row, D) : 0) + c * 8;
-        uint8_t* dst = q + (row / kB) * kB * D * 2 + tile_at(row % kB, c, kB);
-        if (async) copy16(smem_u32(dst), src, there);
-        else *reinterpret_cast<uint4*>(dst) = there ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
-    }
-}
-
-// Loader warps of bf16 caches (128 threads): 16-byte asynchronous copies that
-// arrive on the stage's barrier when they land.
-template <int D, int NS, int QR, typename Order>
-__device__ __forceinline__ void load_bf16(const TreeParams& p, const TcRing& m, const Waiter& wait, TreeCursor cur,
-                                          long long u, long long end, int tid) {
-    constexpr int kChunks = D / 8, kStep = 128 / kChunks;  // rows the threads cover at a time
-    const int c = tid % kChunks, r0 = tid / kChunks;
+// One warp brings the token tiles of the CTA's pieces into slots, in ring order,
+// by tensor copies of boxes of 128 bytes (64 channels; 8-bit: all, 64 of them
+// filled up with zeros, which keeps every row on the 128-byte boundary that a
+// copy needs) and 128 rows, or as many rows as a page has: a lane a page. Rows
+// past the sequence are whatever the cache (or, where a page is not needed, the
+// slot) holds.
+template <int TYPE, int D, int NS, typename Order>
+__device__ __forceinline__ void copy_tiles(const TreeParams& p, const CUtensorMap* mk, const CUtensorMap* mv,
+                                           uint8_t* slots, uint64_t* full, uint64_t* empty, const Waiter& wait,
+                                           TreeCursor cur, long long u, long long end) {
+    constexpr bool kQ8 = TYPE == kTreeE4M3;
+    constexpr int kBlocks = kQ8 ? 1 : D / 64, kSlot = kT * 128 * kBlocks;  // boxes of a row; bytes
+    const int lane = lane_id();
+    const bool paged = p.at.block_table != nullptr;
+    const int shift = p.at.page_shift < 7 ? p.at.page_shift : 7;  // rows of a box, where paged
     Ring<NS> ring;
-    uint32_t q_ph = 1;  // the first wait on q_empty passes
+    unsigned issued = 0;
     TreePiece w;
     while (next_piece(p, cur, u, end, w)) {
         if (w.nodes * p.G - w.mt * p.tile_rows <= 0) continue;
         const int n = w.t1 - w.t0, tokens = w.prefix + w.nodes;
-        if (!__all_sync(0xffffffffu, wait(m.q_empty, q_ph))) break;
-        q_ph ^= 1;
-        load_queries<D, QR, 128>(p, w, m.q, tid, true);  // they land with the first K tile
-        bool ok = true;
-        TilePages pages;
-        if (p.at.block_table) pages.load(p.at, w.e, w.t0 * kT, tokens);
+        // the row of this lane's box in a tile (its first one; small pages have more boxes than lanes)
+        auto row_of = [&](int tok) {
+            int blk = __ldg(p.at.block_table + (size_t)w.e * p.at.max_blocks + (tok >> p.at.page_shift));
+            blk = min(max(blk, 0), p.at.num_blocks - 1);
+            return (int)((((long long)blk * p.at.hkv + w.h) << p.at.page_shift) + (tok & ((1 << p.at.page_shift) - 1)));
+        };
+        auto first_row = [&](int k) {
+            const int tok = (w.t0 + Order::use(k, n).i) * kT + (lane << shift);
+            return tok < tokens && (lane << shift) < kT ? row_of(tok) : 0;
+        };
+        int row = paged ? first_row(0) : 0;
         for (int k = 0; k < 2 * n; ++k) {
             const RingUse use = Order::use(k, n);
-            ok = __all_sync(0xffffffffu, wait(m.empty + ring.i, ring.ph ^ 1));
-            if (!ok) break;
-            const uint32_t dst = smem_u32(m.stages + ring.i * (kT * D * 2));
-            const uint16_t* src = static_cast<const uint16_t*>(use.is_v ? p.v : p.k) + c * 8;
             const int tok0 = (w.t0 + use.i) * kT;
-            if (!p.at.block_table) {
-                // one run of rows: constant steps from the first
-                src += (((long long)w.e * p.at.hkv + w.h) * p.at.s_cap + tok0 + r0) * D;
-#pragma unroll
-                for (int x = 0; x < kChunks; ++x)
-                    copy16(dst + tile_at(r0 + x * kStep, c), src + x * kStep * D, tok0 + r0 + x * kStep < tokens);
-            } else {
-#pragma unroll 8
-                for (int x = 0; x < kChunks; ++x) {
-                    const int r = r0 + x * kStep, t = min(tok0 + r, tokens - 1);
-                    const long long row = pages.row(p.at, w.e, w.h, t, r);
-                    copy16(dst + tile_at(r, c), src + row * D, tok0 + r < tokens);
+            if (!__all_sync(0xffffffffu, wait(empty + ring.i, ring.ph ^ 1))) {
+                // copies in flight land before the block leaves
+                for (unsigned x = 1; x <= NS && x <= issued; ++x) {
+                    const unsigned j = issued - x;
+                    mbar_wait_bounded(full + j % NS, j / NS & 1, p.err, 3, 10000000ull);
                 }
-                if (k + 1 < 2 * n) pages.load(p.at, w.e, (w.t0 + Order::use(k + 1, n).i) * kT, tokens);
+                return;
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(m.full + ring.i))
-                         : "memory");
+            ++issued;
+            const CUtensorMap* map = use.is_v ? mv : mk;
+            const uint32_t dst = smem_u32(slots + ring.i * kSlot), bar = smem_u32(full + ring.i);
+            auto box = [&](int r, int y) {  // rows from y on to tile rows from r on
+#pragma unroll
+                for (int c = 0; c < kBlocks; ++c)
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                                 "[%0], [%1, {%2, %3}], [%4];"
+                                 ::"r"(dst + c * (kT * 128) + r * 128), "l"(map), "r"(c * 64), "r"(y), "r"(bar)
+                                 : "memory");
+            };
+            if (!paged) {
+                if (elected()) {
+                    mbar_arrive_expect_tx(full + ring.i, kSlot);
+                    box(0, (int)(((long long)w.e * p.at.hkv + w.h) * p.at.s_cap) + tok0);
+                }
+            } else {
+                const int have = min(tokens - tok0, kT), boxes = (have + (1 << shift) - 1) >> shift;
+                if (elected()) mbar_arrive_expect_tx(full + ring.i, (boxes << shift) * 128 * kBlocks);
+                __syncwarp();
+                for (int b = lane; b < boxes; b += 32) box(b << shift, b < 32 ? row : row_of(tok0 + (b << shift)));
+                if (k + 1 < 2 * n) row = first_row(k + 1);
+            }
             ring.next();
         }
-        if (!ok) break;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Loader warps of 8-bit caches (256 threads): codes come into registers DEPTH
-// tiles ahead, are widened there and stored to their stage (a copy to shared
-// memory first would cost the tile two more passes through it, which is what
-// bounds 8-bit tiles).
-template <int D, int NS, int QR, typename Order, int DEPTH>
-__device__ __forceinline__ void load_e4m3(const TreeParams& p, const TcRing& m, const Waiter& wait, TreeCursor cur,
-                                          long long u, long long end, int tid) {
+// 256 threads widen the 8-bit tiles of NR slots into the ring's NS stages.
+template <int D, int NR, int NS>
+__device__ __forceinline__ void widen_tiles(const TreeParams& p, const uint8_t* slots, uint64_t* slot_full,
+                                            uint64_t* slot_empty, uint8_t* stages, uint64_t* full, uint64_t* empty,
+                                            const Waiter& wait, TreeCursor cur, long long u, long long end, int tid) {
     constexpr int kC8 = D / 16, kMine = kT * kC8 / 256, kStep = 256 / kC8;  // 16-code chunks of a row, of a thread
     const int c = tid % kC8, r0 = tid / kC8;
+    // the order of the two stores keeps eight lanes on different banks
+    const int odd = D == 128 ? c >> 2 : 0, at0 = tile_at(r0, 2 * c + odd), at1 = tile_at(r0, 2 * c + 1 - odd);
+    Ring<NR> raw;
     Ring<NS> ring;
-    uint32_t q_ph = 1;
-    // reads run over the same pieces and tiles, ahead of the widening
-    TreeCursor acur = cur;
-    long long au = u;
-    TreePiece aw, w;
-    int a_n = 0, a_k = 0, n = 0, k = 0;  // tiles of the piece, place in their order
-    bool a_more = true;
-    TilePages pages;  // of the next tile to read
-    auto advance = [&](TreeCursor& cc, long long& uu, TreePiece& ww, int& nn, int& kk) {
-        while (kk >= 2 * nn) {  // the next piece with rows
-            if (!next_piece(p, cc, uu, end, ww)) return false;
-            if (ww.nodes * p.G - ww.mt * p.tile_rows > 0) { nn = ww.t1 - ww.t0; kk = 0; }
-        }
-        return true;
-    };
-    auto read = [&](uint4 (&x)[kMine]) {
-        if (!a_more) return;
-        const int before = a_k;
-        a_more = advance(acur, au, aw, a_n, a_k);
-        if (!a_more) return;
-        const int tokens = aw.prefix + aw.nodes;
-        if (p.at.block_table && (before != a_k || a_k == 0)) pages.load(p.at, aw.e, aw.t0 * kT, tokens);
-        const RingUse use = Order::use(a_k++, a_n);
-        const int tok0 = (aw.t0 + use.i) * kT;
-        const uint8_t* src = static_cast<const uint8_t*>(use.is_v ? p.v : p.k) + c * 16;
+    TreePiece w;
+    while (next_piece(p, cur, u, end, w)) {
+        if (w.nodes * p.G - w.mt * p.tile_rows <= 0) continue;
+        for (int k = 2 * (w.t1 - w.t0); k > 0; --k) {
+            if (!wait(slot_full + raw.i, raw.ph)) return;
+            uint4 x[kMine];
 #pragma unroll
-        for (int y = 0; y < kMine; ++y) {
-            const int r = r0 + y * kStep, t = min(tok0 + r, tokens - 1);
-            const long long row = p.at.block_table ? pages.row(p.at, aw.e, aw.h, t, r)
-                                                   : ((long long)aw.e * p.at.hkv + aw.h) * p.at.s_cap + t;
-            x[y] = tok0 + r < tokens ? ldg_stream16(src + row * D) : make_uint4(0, 0, 0, 0);
-        }
-        if (p.at.block_table && a_k < 2 * a_n) pages.load(p.at, aw.e, (aw.t0 + Order::use(a_k, a_n).i) * kT, tokens);
-    };
-    auto step = [&](uint4 (&x)[kMine]) {  // widens and stores one tile, reads a later one in its place
-        const int before = k;
-        if (!advance(cur, u, w, n, k)) return false;
-        if (before != k || k == 0) {
-            if (!__all_sync(0xffffffffu, wait(m.q_empty, q_ph))) return false;
-            q_ph ^= 1;
-            load_queries<D, QR, 256>(p, w, m.q, tid, false);
-        }
-        ++k;
-        if (!__all_sync(0xffffffffu, wait(m.empty + ring.i, ring.ph ^ 1))) return false;
-        uint8_t* dst = m.stages + ring.i * (kT * D * 2);
+            for (int y = 0; y < kMine; ++y)
+                x[y] = *reinterpret_cast<const uint4*>(slots + raw.i * (kT * 128) + (r0 + y * kStep) * 128 + c * 16);
+            if (!wait(empty + ring.i, ring.ph ^ 1)) return;
+            uint8_t* dst = stages + ring.i * (kT * D * 2);
 #pragma unroll
-        for (int y = 0; y < kMine; ++y) {
-            const int r = r0 + y * kStep;
-            const uint2 a = widen4(x[y].x), b = widen4(x[y].y), d = widen4(x[y].z), f = widen4(x[y].w);
-            *reinterpret_cast<uint4*>(dst + tile_at(r, 2 * c)) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4*>(dst + tile_at(r, 2 * c + 1)) = make_uint4(d.x, d.y, f.x, f.y);
+            for (int y = 0; y < kMine; ++y) {  // (kStep is a multiple of 8: the rows' places differ by whole groups)
+                const uint2 a = widen4(x[y].x), b = widen4(x[y].y), d = widen4(x[y].z), f = widen4(x[y].w);
+                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, f.x, f.y);
+                *reinterpret_cast<uint4*>(dst + at0 + y * kStep * 128) = odd ? hi : lo;
+                *reinterpret_cast<uint4*>(dst + at1 + y * kStep * 128) = odd ? lo : hi;
+            }
+            mbar_arrive(slot_empty + raw.i);
+            proxy_fence();
+            mbar_arrive(full + ring.i);
+            raw.next();
+            ring.next();
+        }
+    }
+}
+
+// 64 threads bring a piece's queries: QR rows in blocks of at most 128, zeros
+// past its own.
+template <int D, int QR>
+__device__ __forceinline__ void copy_queries(const TreeParams& p, uint8_t* q, uint64_t* q_full, uint64_t* q_empty,
+                                             const Waiter& wait, TreeCursor cur, long long u, long long end, int tid) {
+    constexpr int kChunks = D / 8, kB = QR < kT ? QR : kT;
+    uint32_t ph = 1;  // the first wait passes
+    TreePiece w;
+    while (next_piece(p, cur, u, end, w)) {
+        const int row0 = w.mt * p.tile_rows, rows = w.nodes * p.G - row0;
+        if (rows <= 0) continue;
+        if (!wait(q_empty, ph)) return;
+        ph ^= 1;
+#pragma unroll 8
+        for (int x = tid; x < QR * kChunks; x += 64) {
+            const int row = x / kChunks, c = x % kChunks;
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (row < rows)
+                y = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                         q_offset(p, w.e, w.h, row0 + row, D) + c * 8));
+            *reinterpret_cast<uint4*>(q + (row / kB) * kB * D * 2 + tile_at(row % kB, c, kB)) = y;
         }
         proxy_fence();
-        mbar_arrive(m.full + ring.i);
-        ring.next();
-        read(x);
-        return true;
-    };
-    uint4 x[DEPTH][kMine];
-#pragma unroll
-    for (int y = 0; y < DEPTH; ++y) read(x[y]);
-    for (bool ok = true; ok;) {
-#pragma unroll
-        for (int y = 0; y < DEPTH; ++y) {
-            ok = step(x[y]);
-            if (!ok) break;
-        }
+        mbar_arrive(q_full);
     }
 }
 
 }  // namespace
+
+// Tensor maps of the caches for copy_tiles (ds_tree_tc.cu).
+struct TreeMaps { CUtensorMap k, v; };
+cudaError_t make_tree_maps(const TreeParams& p, int type, int d, TreeMaps* m);
 
 }  // namespace ds

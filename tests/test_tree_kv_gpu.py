@@ -112,6 +112,16 @@ TREE = [
     ("e4m3", 2, 40, 15, 3, 64, 200, None, 1, "tree"),
     ("e4m3", 1, 64, 8, 1, 128, 390, None, 64, "tree"),
     ("e4m3", 5, 5, 4, 4, 64, 130, [0, 1, 123, 124, 130], 8, "tree"),
+    ("bf16", 2, 6, 4, 2, 128, 333, [333, 40], 1, "tree"),
+    ("bf16", 2, 11, 8, 2, 128, 300, None, 2, "tree"),
+    ("bf16", 1, 9, 10, 2, 64, 260, None, 4, "tree"),
+    ("bf16", 2, 20, 6, 2, 64, 500, [500, 130], 8, "tree"),
+    ("bf16", 1, 17, 14, 2, 64, 777, None, 0, "tree"),
+    ("e4m3", 2, 3, 4, 2, 64, 333, [333, 40], 1, "tree"),
+    ("e4m3", 1, 10, 6, 2, 128, 300, None, 2, "tree"),
+    ("e4m3", 2, 21, 6, 2, 128, 640, [640, 130], 32, "tree"),
+    ("e4m3", 1, 33, 2, 2, 64, 1024, None, 0, "tree"),
+    ("e4m3", 1, 40, 6, 2, 64, 1024, None, 4, "tree"),
 ]
 
 
