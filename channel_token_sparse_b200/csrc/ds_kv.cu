@@ -34,6 +34,13 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+// x / s correctly rounded, from r = 1 / s correctly rounded (Markstein 1990:
+// one residual corrects the product), for quotients that do not underflow; a
+// division instruction sequence each was what bounded 8-bit writes.
+__device__ __forceinline__ float divide(float x, float s, float r) {
+    const float q = __fmul_rn(x, r);
+    return fmaf(fmaf(-q, s, x), r, q);
+}
 // Maximum that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -176,11 +183,12 @@ __global__ void __launch_bounds__(kKvNT) ds_write_kv_kernel(const WriteArgs a, i
         if constexpr (Q8) {
             float sc = max_nan(__fdiv_rn(amax, 448.f), 1.17549435e-38f);
             sc = fmaf(sc, 0.f, sc);  // an infinite scale becomes NaN: the row reads back as NaN
+            const float rs = __frcp_rn(sc);
             uint32_t w0[2] = {0, 0}, w1[2] = {0, 0};
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
-                w0[j / 4] |= e4m3x2(__fdiv_rn(x0[j], sc), __fdiv_rn(x0[j + 1], sc)) << (8 * (j & 3));
-                w1[j / 4] |= e4m3x2(__fdiv_rn(x1[j], sc), __fdiv_rn(x1[j + 1], sc)) << (8 * (j & 3));
+                w0[j / 4] |= e4m3x2(divide(x0[j], sc, rs), divide(x0[j + 1], sc, rs)) << (8 * (j & 3));
+                w1[j / 4] |= e4m3x2(divide(x1[j], sc, rs), divide(x1[j + 1], sc, rs)) << (8 * (j & 3));
             }
             uint8_t* out = static_cast<uint8_t*>(kind == 1 ? a.k_cache : a.v_cache) + r * D;
             *reinterpret_cast<uint2*>(out + c0) = make_uint2(w0[0], w0[1]);

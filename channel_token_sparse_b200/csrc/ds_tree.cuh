@@ -214,7 +214,7 @@ enum TreeType { kTreeF32 = 0, kTreeBF16 = 1, kTreeE4M3 = 2 };
 struct TreePlan { int tile_rows, tile_tokens, grid; };
 TreePlan plan_tree_simt(int rows, int d);
 cudaError_t launch_tree_simt(const TreeParams& p, int d, cudaStream_t st);
-// bf16 and e4m3 (ds_tree_tc.cu; up to 64 query rows: ds_tree_few.cu).
+// bf16 and e4m3 (ds_tree_tc.cu; up to 32 query rows: ds_tree_few.cu).
 TreePlan plan_tree_tc(int rows, int d);
 cudaError_t launch_tree_tc(const TreeParams& p, int type, int d, cudaStream_t st);
 cudaError_t launch_tree_combine(const TreeParams& p, int d, cudaStream_t st);

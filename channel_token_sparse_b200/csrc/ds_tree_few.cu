@@ -1,9 +1,9 @@
-// ds_tree_few.cu -- tree attention of up to 64 query rows a kv head over bf16
+// ds_tree_few.cu -- tree attention of up to 32 query rows a kv head over bf16
 // and 8-bit caches, on the tensor cores, for sm_100a.
 //
 // The products are taken the other way round from ds_tree_tc.cu: S^T = K Q^T
 // and O^T += V^T P^T, so that the 128 rows the tensor cores want are the
-// tile's tokens (then the channels) and N = 16, 32 or 64 covers the query
+// tile's tokens (then the channels) and N = 16 or 32 covers the query
 // rows. With few rows this is what keeps the kernel at the cache's bandwidth:
 // a tile costs N / 128 of the products and of the exponentials, a thread has
 // one token and N of them (rather than one row and 128), and an 8-bit row's
@@ -42,7 +42,9 @@ struct Cfg {
     static constexpr int kBars = 2 * kStages + 2 * kRaw + 12;
     static constexpr int kSmem = oBar + kBars * 8 + 64;
     static_assert(kSmem <= 227 * 1024 && kQ % 1024 == 0, "shared memory");
-    static constexpr int kCols = N == 64 ? 512 : N == 32 ? 256 : 128;  // tensor memory: 4 S^T, 2 O^T of N columns
+    // K_i and V_i are five uses of the ring apart at most: see the tidying
+    static_assert(kQ8 || kStages >= 5, "stages");
+    static constexpr int kCols = N == 32 ? 256 : 128;  // tensor memory: 4 S^T, 2 O^T of N columns
 };
 
 // K0 K1, then K_{i+2} V_i.
@@ -115,21 +117,21 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, C::kQ8 ? 256 : 1);
+            mbar_init(full + i, C::kQ8 ? 4 : 1);
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < C::kRaw; ++i) {
             mbar_init(raw_full + i, 1);
-            mbar_init(raw_empty + i, 256);
+            mbar_init(raw_empty + i, 4);
         }
         for (int s = 0; s < 4; ++s) mbar_init(s_full + s, 1);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(p_full + s, 128);
+            mbar_init(p_full + s, 4);
             mbar_init(o_done + s, 1);
         }
         mbar_init(q_empty, 1);
-        mbar_init(q_full, 64);
-        mbar_init(xch, 256);
+        mbar_init(q_full, 2);
+        mbar_init(xch, 8);
         mbar_init(drain, 1);
         *stop = 0;
         for (int i = 0; i < 8; ++i) bad[i] = 0;
@@ -170,33 +172,38 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
             else
                 copy_tiles<TYPE, D, NS, FewOrder>(p, &maps.k, &maps.v, smem + C::oStage, full, empty, wait, cur, u, end);
         } else if (warp >= 10) {
-            copy_queries<D, N>(p, smem, q_full, q_empty, wait, cur, u, end, threadIdx.x - 10 * 32);
+            copy_queries<D, N, C::kQ8>(p, smem, q_full, q_empty, wait, cur, u, end, threadIdx.x - 10 * 32);
         }
-        if (warp > 8) u = end;  // the products are warp 8's
+        // The products are warp 8's. What their operands and loops depend on comes
+        // from votes and reductions, so that it lives in uniform registers: moved
+        // there for each instruction, it made a product take 125 cycles to issue.
+        const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
         Ring<NS> ring;
         uint32_t p_ph[2] = {0, 0}, q_ph = 0;
         constexpr uint32_t kS = instr_desc(N, false, false), kO = instr_desc(N, true, true);
         const uint32_t q_addr = smem_u32(smem), p_addr = smem_u32(smem + C::oP), st_addr = smem_u32(smem + C::oStage);
-        auto commit = [&](uint64_t* bar) { if (elected()) tc_commit(bar); };
-        while (next_piece(p, cur, u, end, w)) {
-            if (w.nodes * p.G - w.mt * p.tile_rows <= 0) continue;
-            const int n = w.t1 - w.t0;
+        auto all_spin = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait.spin(bar, parity)) != 0; };
+        while (warp == 8) {
+            const bool more = next_piece(p, cur, u, end, w);
+            if (!__any_sync(0xffffffffu, more)) break;
+            if (!__any_sync(0xffffffffu, w.nodes * p.G - w.mt * p.tile_rows > 0)) continue;
+            const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)(w.t1 - w.t0));
             bool ok = all_wait(q_full, q_ph);
             q_ph ^= 1;
             // S^T of tile i + 2, then PV of tile i
             for (int i = -2; ok && i < n; ++i) {
                 const int s = i & 1;
                 if (i + 2 < n) {
-                    ok = all_wait(full + ring.i, ring.ph);
+                    ok = all_spin(full + ring.i, ring.ph);
                     if (!ok) break;
                     const int b = 2 * s + (((i + 2) >> 1) & 1);
-                    const uint32_t d = tmem + b * N;
+                    const uint32_t d = tm + b * N;
                     const uint64_t ka = smem_desc(st_addr + ring.i * C::kStage, 16, 1024), qb = smem_desc(q_addr, 16, 1024);
-                    if (elected()) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            mma_ss(d, ka + (((k >> 2) * (kT * 128) + (k & 3) * 32) >> 4),
-                                   qb + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), kS, k > 0);
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(d, ka, ((k >> 2) * (kT * 128) + (k & 3) * 32) >> 4, qb,
+                               ((k >> 2) * (N * 128) + (k & 3) * 32) >> 4, kS, k > 0);
+                    if (elected()) {
                         tc_commit(s_full + b);
                         tc_commit(empty + ring.i);
                         if (i + 3 == n) tc_commit(q_empty);
@@ -204,17 +211,17 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                     ring.next();
                 }
                 if (i >= 0) {
-                    ok = all_wait(full + ring.i, ring.ph) && all_wait(p_full + s, p_ph[s]);
+                    ok = all_spin(full + ring.i, ring.ph) && all_spin(p_full + s, p_ph[s]);
                     if (!ok) break;
                     p_ph[s] ^= 1;
                     tc_fence_after();
-                    const uint32_t d = tmem + 4 * N + s * N;
+                    const uint32_t d = tm + 4 * N + s * N;
                     // (64 channels: the other 64 rows repeat them)
                     const uint64_t va = smem_desc(st_addr + ring.i * C::kStage, D == 128 ? kT * 128 : 0, 1024);
                     const uint64_t pb = smem_desc(p_addr + s * C::kP, 16, 1024);
-                    if (elected()) {
 #pragma unroll
-                        for (int k = 0; k < kT / 16; ++k) mma_ss(d, va + k * 128, pb + k * 128, kO, i >= 2 || k > 0);
+                    for (int k = 0; k < kT / 16; ++k) mma_ss(d, va, k * 128, pb, k * 128, kO, i >= 2 || k > 0);
+                    if (elected()) {
                         tc_commit(o_done + s);
                         tc_commit(empty + ring.i);
                     }
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                 }
             }
             if (!ok) {  // products in flight end before the tensor memory is given back
-                commit(drain);
+                if (elected()) tc_commit(drain);
                 mbar_wait_bounded(drain, 0, p.err, 3, 10000000ull);
                 break;
             }
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
     } else {
         // ------------------------------------------------------------ softmax
         reg_inc<C::kRegSoftmax>();
-        constexpr int HN = N == 64 || (C::kQ8 && N == 32) ? 16 : N, H = N / HN;  // columns a thread holds at a time
+        constexpr int HN = C::kQ8 ? 16 : N, H = N / HN;  // columns a thread holds at a time
         const int st = warp >> 2, bar = 1 + st;         // stream, its barrier
         const int t = threadIdx.x & 127;                // token of a tile; channel of O^T
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -271,27 +278,29 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                     }
                 }
                 bool fine = true;
-                unsigned long long vis = ~0ull;  // query rows that see this token
+                uint32_t vis = ~0u;  // query rows that see this token
                 if (masked) {
                     if (node_t >= w.nodes) vis = 0;
                     else if (node_t >= 0) {
                         vis = 0;
-                        const unsigned long long g = (1ull << p.G) - 1;
+                        const uint32_t g = (1u << p.G) - 1;
                         for (int r = 0, x = row0 / p.G; r < rows; ++x, r += p.G)
                             if (mask_word(p, w.e, x, node_t >> 5) >> (node_t & 31) & 1) vis |= g << r;
                     }
                 }
+                const int buf = (i >> 1) & 1;
+                fine = __all_sync(0xffffffffu, wait.spin(s_full + 2 * st + buf, s_ph[buf])) && fine;
+                s_ph[buf] ^= 1;
                 if (masked && !C::kQ8) {
-                    // the stage is tidied first (see ds_tree_tc.cu)
+                    // The V stage is tidied (see ds_tree_tc.cu). Only now: while S^T was not
+                    // there, the stage's use before could still be landing, and the parity
+                    // of this one's phase would be that of two before.
                     const unsigned use = uses + FewOrder::v_use(i, n), stage = use % NS;
-                    fine = all_wait(full + stage, use / NS & 1);
+                    fine = all_wait(full + stage, use / NS & 1) && fine;
                     if (fine)
                         tidy_values<D>(smem + C::oStage + stage * C::kStage, max(w.prefix - tok0, 0),
                                        min(tokens - tok0, kT), tok0 - w.prefix, bad, t);
                 }
-                const int buf = (i >> 1) & 1;
-                fine = all_wait(s_full + 2 * st + buf, s_ph[buf]) && fine;
-                s_ph[buf] ^= 1;
                 if (done > 0) fine = all_wait(o_done + st, (o_cnt - 1) & 1) && fine;  // P^T and O^T are free
                 tc_fence_after();
                 float x[HN];
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                 }
                 proxy_fence();
                 tc_fence_before();
-                mbar_arrive(p_full + st);
+                warp_arrive(p_full + st);
                 if (C::kQ8 && i + 2 < n) scales(tok0 + 2 * kT + t);  // (before, the fence would wait for them)
                 ++o_cnt;
                 ++done;
@@ -400,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
             }
             if (done == 0 && t < N) mx[t] = kFloor;
             tc_fence_before();
-            mbar_arrive(xch);
+            warp_arrive(xch);
             ok = group_wait(xch, x_ph);
             if (!ok) break;
             x_ph ^= 1;
@@ -425,12 +434,12 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                     part[p.part_rows + r] = sum;
                 }
             }
-            mbar_arrive(xch);
+            warp_arrive(xch);
             ok = group_wait(xch, x_ph);
             if (!ok) break;
             x_ph ^= 1;
             // a thread has one channel of O^T, and half of the rows
-            const int first = st * (N / 2);
+            const int first = st * (N / 2), ch = C::kQ8 ? widened_channel(t) : t;
             constexpr int kG = N / 2 < 16 ? N / 2 : 16;
             const int warp_c = (warp & 3) * 32;
             if (warp_c < D) {
@@ -447,9 +456,9 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                         if (n > 1) o = fmaf(b[c], s_fin[N + r], o);
                         o *= s_fin[2 * N + r];
                         if (!whole) {
-                            part[2 * p.part_rows + (size_t)r * D + t] = o;
+                            part[2 * p.part_rows + (size_t)r * D + ch] = o;
                         } else {
-                            const size_t at = q_offset(p, w.e, w.h, row0 + r, D) + t;
+                            const size_t at = q_offset(p, w.e, w.h, row0 + r, D) + ch;
                             if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
                             else static_cast<float*>(p.out)[at] = o;
                         }
@@ -459,20 +468,20 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
             if (any_bad && warp_c < D) {
 #pragma unroll 1
                 for (int r = first; r < min(first + N / 2, rows); ++r) {
-                    const float f = not_finite_seen<TYPE, D>(p, w, (row0 + r) / p.G, bad, t);
+                    const float f = not_finite_seen<TYPE, D>(p, w, (row0 + r) / p.G, bad, ch);
                     add_result(p, whole ? nullptr : part + 2 * p.part_rows,
-                               whole ? q_offset(p, w.e, w.h, row0 + r, D) + t : (size_t)r * D + t, f);
+                               whole ? q_offset(p, w.e, w.h, row0 + r, D) + ch : (size_t)r * D + ch, f);
                 }
             }
             // both streams have read O^T, the statistics and the marks before either goes on
             tc_fence_before();
-            mbar_arrive(xch);
+            warp_arrive(xch);
             ok = group_wait(xch, x_ph);
             if (!ok) break;
             x_ph ^= 1;
             if (any_bad) {  // cleared before the next piece marks
                 if (threadIdx.x < 8) bad[threadIdx.x] = 0;
-                mbar_arrive(xch);
+                warp_arrive(xch);
                 ok = group_wait(xch, x_ph);
                 if (!ok) break;
                 x_ph ^= 1;
@@ -501,7 +510,7 @@ cudaError_t run(const TreeParams& p, const TreeMaps& m, cudaStream_t st) {
 
 cudaError_t launch_tree_few(const TreeParams& p, const TreeMaps& m, int type, int d, cudaStream_t st) {
 #define DS_N(TY, D_) \
-    (p.tile_rows == 16 ? run<TY, D_, 16>(p, m, st) : p.tile_rows == 32 ? run<TY, D_, 32>(p, m, st) : run<TY, D_, 64>(p, m, st))
+    (p.tile_rows == 16 ? run<TY, D_, 16>(p, m, st) : run<TY, D_, 32>(p, m, st))
     if (type == kTreeBF16) return d == 64 ? DS_N(kTreeBF16, 64) : DS_N(kTreeBF16, 128);
     return d == 64 ? DS_N(kTreeE4M3, 64) : DS_N(kTreeE4M3, 128);
 #undef DS_N

@@ -42,9 +42,9 @@ struct Cfg {
     static_assert(kQ8 ? 2 * kRegSoftmax + kRegMma + 2 * kRegWiden <= 5 * 96 : 2 * kRegSoftmax + kRegMma <= 3 * 168, "");
     static constexpr int kStage = kT * D * 2;       // bytes of a K or V tile in bf16
     static constexpr int kQ = MT * kT * D * 2;
-    static constexpr int kRaw = kQ8 ? 3 : 0, kRawBytes = kT * 128;  // slots of 8-bit tiles
+    static constexpr int kRaw = kQ8 ? (D == 128 && MT == 2 ? 2 : 4) : 0, kRawBytes = kT * 128;  // slots of 8-bit tiles
     static constexpr int kScale = kQ8 ? 8 * 2 * kT * 4 : 0;  // a softmax warp's K and V scales of a tile
-    static constexpr int kStages = D == 128 ? 7 - MT - 2 * kQ8 : 13 - MT - 4 * kQ8;
+    static constexpr int kStages = D == 128 ? (kQ8 ? 3 : 7 - MT) : 13 - MT - 4 * kQ8;
     static constexpr int oStage = kQ, oRaw = oStage + kStages * kStage, oScale = oRaw + kRaw * kRawBytes;
     static constexpr int oMl = oScale + kScale;             // [2][128] maxima, [2][128] sums
     static constexpr int oBar = oMl + 4 * kT * 4;
@@ -96,21 +96,21 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, C::kQ8 ? 256 : 1);
+            mbar_init(full + i, C::kQ8 ? 4 : 1);
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < C::kRaw; ++i) {
             mbar_init(raw_full + i, 1);
-            mbar_init(raw_empty + i, 256);
+            mbar_init(raw_empty + i, 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + s, 1);
-            mbar_init(p_full + s, 128);
+            mbar_init(p_full + s, 4);
             mbar_init(o_done + s, 1);
         }
         mbar_init(q_empty, 1);
-        mbar_init(q_full, 64);
-        mbar_init(xch, 256);
+        mbar_init(q_full, 2);
+        mbar_init(xch, 8);
         mbar_init(drain, 1);
         *stop = 0;
         for (int i = 0; i < 8; ++i) bad[i] = 0;
@@ -150,40 +150,38 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             else
                 copy_tiles<TYPE, D, NS, TcOrder<MT>>(p, &maps.k, &maps.v, smem + C::oStage, full, empty, wait, cur, u, end);
         } else if (warp >= 10) {
-            copy_queries<D, MT * kT>(p, smem, q_full, q_empty, wait, cur, u, end, threadIdx.x - 10 * 32);
+            copy_queries<D, MT * kT, C::kQ8>(p, smem, q_full, q_empty, wait, cur, u, end, threadIdx.x - 10 * 32);
         }
-        if (warp > 8) u = end;  // the products are warp 8's
+        // The products are warp 8's. What their operands and loops depend on comes
+        // from votes and reductions, so that it lives in uniform registers: moved
+        // there for each instruction, it made a product take 125 cycles to issue.
+        const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
         Ring<NS> ring;
         uint32_t p_ph[2] = {0, 0}, q_ph = 0;
         constexpr uint32_t kS = instr_desc(kT, false, false), kO = instr_desc(D, false, true);
         const uint32_t q_addr = smem_u32(smem), st_addr = smem_u32(smem + C::oStage);
-        auto s_of = [&](int s) { return tmem + s * kT; };
-        auto o_of = [&](int s) { return tmem + 2 * kT + s * D; };
-        // The whole warp walks along, so addresses stay warp-uniform; one lane issues.
-        auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+        auto s_of = [&](int s) { return tm + s * kT; };
+        auto o_of = [&](int s) { return tm + 2 * kT + s * D; };
+        auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait.spin(bar, parity)) != 0; };
         auto ready = [&](const Ring<NS>& r) { return all_wait(full + r.i, r.ph); };
         auto commit = [&](uint64_t* bar) { if (elected()) tc_commit(bar); };
         auto scores = [&](int s, int stage) {  // S = Q K^T of stream s
             const uint32_t d = s_of(s);
             const uint64_t a = smem_desc(q_addr + (MT == 2 ? s : 0) * kT * D * 2, 16, 1024);
             const uint64_t b = smem_desc(st_addr + stage * C::kStage, 16, 1024);
-            if (elected()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * (kT * 128) + (k & 3) * 32) >> 4;
-                    mma_ss(d, a + off, b + off, kS, k > 0);
-                }
-                tc_commit(s_full + s);
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * (kT * 128) + (k & 3) * 32) >> 4;
+                mma_ss(d, a, off, b, off, kS, k > 0);
             }
+            commit(s_full + s);
         };
         auto values = [&](int s, int stage, bool add) {  // O += P V of stream s
             const uint32_t d = o_of(s), a = s_of(s);
             const uint64_t b = smem_desc(st_addr + stage * C::kStage, kT * 128, 1024);
-            if (elected()) {
 #pragma unroll
-                for (int k = 0; k < kT / 16; ++k) mma_ts(d, a + k * 8, b + k * 128, kO, add || k > 0);
-                tc_commit(o_done + s);
-            }
+            for (int k = 0; k < kT / 16; ++k) mma_ts(d, a + k * 8, b, k * 128, kO, add || k > 0);
+            commit(o_done + s);
         };
         auto weights = [&](int s) {  // P of stream s is there
             if (!all_wait(p_full + s, p_ph[s])) return false;
@@ -191,24 +189,27 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             tc_fence_after();
             return true;
         };
-        while (next_piece(p, cur, u, end, w)) {
-            if (w.nodes * p.G - w.mt * p.tile_rows <= 0) continue;
-            const int n = w.t1 - w.t0;
+        while (warp == 8) {
+            const bool any = next_piece(p, cur, u, end, w);
+            if (!__any_sync(0xffffffffu, any)) break;
+            if (!__any_sync(0xffffffffu, w.nodes * p.G - w.mt * p.tile_rows > 0)) continue;
+            const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)(w.t1 - w.t0));
             bool ok = all_wait(q_full, q_ph);
             q_ph ^= 1;
             if (MT == 1) {
                 // S of the first two tiles, then PV of tile i and S of tile i + 2
                 for (int i = -2; ok && i < n; ++i) {
-                    if (i >= 0) {
-                        ok = ready(ring) && weights(i & 1);
+                    const Ring<NS> rv = ring;
+                    if (i >= 0) ring.next();
+                    // both tiles first: they are there long before the weights
+                    ok = (i < 0 || ready(rv)) && (i + 2 >= n || ready(ring));
+                    if (ok && i >= 0) {
+                        ok = weights(i & 1);
                         if (!ok) break;
-                        values(i & 1, ring.i, i >= 2);
-                        commit(empty + ring.i);
-                        ring.next();
+                        values(i & 1, rv.i, i >= 2);
+                        commit(empty + rv.i);
                     }
-                    if (i + 2 < n) {
-                        ok = ready(ring);
-                        if (!ok) break;
+                    if (ok && i + 2 < n) {
                         scores(i & 1, ring.i);
                         commit(empty + ring.i);
                         if (i + 3 == n) commit(q_empty);
@@ -218,21 +219,20 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             } else {
                 // of each stream: PV of tile i, then S of tile i + 1
                 Ring<NS> rv = ring;
-                for (int i = -1; ok && i < n; ++i) {
+                for (int i = -1; i < n; ++i) {
                     const bool more = i + 1 < n;
                     if (i >= 0) { rv = ring; ring.next(); }
+                    // both tiles first: they are there long before the weights
+                    ok = (i < 0 || ready(rv)) && (!more || ready(ring));
+                    if (!ok) break;
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         if (i >= 0) {
-                            ok = (s > 0 || ready(rv)) && weights(s);
+                            ok = weights(s);
                             if (!ok) break;
                             values(s, rv.i, i > 0);
                         }
-                        if (more) {
-                            ok = s > 0 || ready(ring);
-                            if (!ok) break;
-                            scores(s, ring.i);
-                        }
+                        if (more) scores(s, ring.i);
                     }
                     if (!ok) break;
                     if (i >= 0) commit(empty + rv.i);
@@ -307,8 +307,13 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                     }
                     __syncwarp();
                 }
+                ok = __all_sync(0xffffffffu, wait.spin(s_full + st, s_ph));
+                if (!ok) break;
+                s_ph ^= 1;
                 if (masked && !C::kQ8) {
-                    // the stage is tidied before the products read it (see the top)
+                    // The V stage is tidied before the products read it (see the top). Only now:
+                    // while S was not there, the stage's use before could still be landing, and
+                    // the parity of this one's phase would be that of two before.
                     const unsigned use = uses + TcOrder<MT>::v_use(i, n), stage = use % NS;
                     ok = all_wait(full + stage, use / NS & 1);
                     if (!ok) break;
@@ -316,9 +321,6 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                                    tok0 - w.prefix, bad, threadIdx.x & 127);
                     proxy_fence();
                 }
-                ok = all_wait(s_full + st, s_ph);
-                if (!ok) break;
-                s_ph ^= 1;
                 tc_fence_after();
                 if (warp_live) {
                     if (masked) {  // what a row does not see gets the score -infinity
@@ -343,26 +345,34 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                             __syncwarp();
                         }
                     }
-                    // the tile's maximum
+                    // The tile's maximum. MT = 2, where the softmax is on the critical path:
+                    // the scores stay in registers from here on (64 nodes over 128K: 217 ->
+                    // 210 us; one row block is 6 % slower so); else they are read once more.
+                    constexpr int kHeld = C::kQ8 || MT == 1 ? 2 : 4;
+                    uint32_t x[kHeld][32];
                     float mx = -INFINITY;
 #pragma unroll 1
-                    for (int k = 0; k < 4; k += 2) {
-                        uint32_t x[2][32];
-                        tc_ld(x[0], t_s + 32 * k);
-                        tc_ld(x[1], t_s + 32 * k + 32);
+                    for (int k = 0; k < 4; k += kHeld) {
+#pragma unroll
+                        for (int h = 0; h < kHeld; ++h) tc_ld(x[h], t_s + 32 * (k + h));
                         tc_wait_ld();
                         float a[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int j = 0; j < 64; j += 4) {
-                            float f[4];
+                        for (int h = 0; h < kHeld; ++h) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) f[q] = __uint_as_float(x[j >> 5][(j & 31) + q]);
-                            if constexpr (C::kQ8) {
-                                const float4 sc = *reinterpret_cast<const float4*>(ks + 32 * k + j);
-                                f[0] *= sc.x; f[1] *= sc.y; f[2] *= sc.z; f[3] *= sc.w;
+                            for (int j = 0; j < 32; j += 8) {
+                                float f[8];
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) f[q] = __uint_as_float(x[h][j + q]);
+                                if constexpr (C::kQ8) {
+                                    const float4 s0 = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j);
+                                    const float4 s1 = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j + 4);
+                                    f[0] *= s0.x; f[1] *= s0.y; f[2] *= s0.z; f[3] *= s0.w;
+                                    f[4] *= s1.x; f[5] *= s1.y; f[6] *= s1.z; f[7] *= s1.w;
+                                }
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) a[q] = fmaxf(fmaxf(a[q], f[2 * q]), f[2 * q + 1]);
                             }
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) a[q] = fmaxf(a[q], f[q]);
                         }
                         mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                     }
@@ -381,25 +391,26 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                             l *= f;
 #pragma unroll
                             for (int k = 0; k < D / 32; ++k) {
-                                uint32_t x[32];
-                                tc_ld(x, t_o + st * D + 32 * k);
+                                uint32_t y[32];
+                                tc_ld(y, t_o + st * D + 32 * k);
                                 tc_wait_ld();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                                tc_st(t_o + st * D + 32 * k, x);
+                                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                                tc_st(t_o + st * D + 32 * k, y);
                             }
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : -m;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-                    for (int k = 0; k < 4; k += 2) {
-                        uint32_t x[2][32];
-                        tc_ld(x[0], t_s + 32 * k);
-                        tc_ld(x[1], t_s + 32 * k + 32);
-                        tc_wait_ld();
+                    for (int k = 0; k < 4; k += kHeld) {
+                        if constexpr (kHeld < 4) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                            for (int h = 0; h < kHeld; ++h) tc_ld(x[h], t_s + 32 * (k + h));
+                            tc_wait_ld();
+                        }
+#pragma unroll
+                        for (int h = 0; h < kHeld; ++h) {
                             uint32_t y[16];
 #pragma unroll
                             for (int j = 0; j < 32; j += 4) {
@@ -411,14 +422,13 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                                     f[0] = fmaf(f[0], sc.x, base); f[1] = fmaf(f[1], sc.y, base);
                                     f[2] = fmaf(f[2], sc.z, base); f[3] = fmaf(f[3], sc.w, base);
                                 } else {
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q) f[q] = fmaf(f[q], p.qscale, base);
+                                    fma2(f[0], f[1], p.qscale, base);
+                                    fma2(f[2], f[3], p.qscale, base);
                                 }
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    f[q] = ex2(f[q]);
-                                    sum[q] += f[q];
-                                }
+                                for (int q = 0; q < 4; ++q) f[q] = ex2(f[q]);
+                                add2(sum[0], sum[1], f[0], f[1]);
+                                add2(sum[2], sum[3], f[2], f[3]);
                                 if constexpr (C::kQ8) {
                                     const float4 sc = *reinterpret_cast<const float4*>(vs + 32 * (k + h) + j);
                                     f[0] *= sc.x; f[1] *= sc.y; f[2] *= sc.z; f[3] *= sc.w;
@@ -433,7 +443,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                     tc_wait_st();
                 }
                 tc_fence_before();
-                mbar_arrive(p_full + st);
+                warp_arrive(p_full + st);
                 if (C::kQ8 && i + kEvery < n) scales(tok0 + kEvery * kT);
                 ++o_cnt;
                 ++done;
@@ -448,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             ml[st * kT + r] = m;
             ml[(2 + st) * kT + r] = l;
             tc_fence_before();
-            mbar_arrive(xch);
+            warp_arrive(xch);
             ok = all_wait(xch, x_ph);
             if (!ok) break;
             x_ph ^= 1;
@@ -493,6 +503,14 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(x[j]), f1, o[j]);
                     }
+                    if constexpr (C::kQ8) {  // channels back in their order
+#pragma unroll
+                        for (int j = 1; j < 32; j += 4) {
+                            const float y = o[j];
+                            o[j] = o[j + 1];
+                            o[j + 1] = y;
+                        }
+                    }
                     if (!live) continue;
                     if (!whole) {
                         float4* d = reinterpret_cast<float4*>(part + 2 * p.part_rows + (size_t)item_row * D + col);
@@ -522,13 +540,13 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             }
             // both streams have read O, the maxima and the marks before either goes on
             tc_fence_before();
-            mbar_arrive(xch);
+            warp_arrive(xch);
             ok = all_wait(xch, x_ph);
             if (!ok) break;
             x_ph ^= 1;
             if (any_bad && threadIdx.x < 8) bad[threadIdx.x] = 0;
             if (any_bad) {  // cleared before the next piece marks
-                mbar_arrive(xch);
+                warp_arrive(xch);
                 ok = all_wait(xch, x_ph);
                 x_ph ^= 1;
             }
@@ -585,7 +603,10 @@ cudaError_t make_tree_maps(const TreeParams& p, int type, int d, TreeMaps* m) {
 
 TreePlan plan_tree_tc(int rows, int d) {
     (void)d;
-    const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= kT ? kT : 2 * kT;
+    // Up to 32 query rows the products with tokens as rows (ds_tree_few.cu) are
+    // faster: 28 rows, 16 x 8K bf16 in pages, step of 92 us against 98; with 64
+    // rows, 4 x 32K, they took 136 us against 117.
+    const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kT ? kT : 2 * kT;
     return TreePlan{tile, kT, 148};
 }
 

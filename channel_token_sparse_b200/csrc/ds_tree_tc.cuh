@@ -81,21 +81,30 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool a_m_major, 
     return 1u << 4 | 1u << 7 | 1u << 10 | (a_m_major ? 1u << 15 : 0u) | (b_n_major ? 1u << 16 : 0u) |
            (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
-}
 // One lane of the warp, the same one every time.
 __device__ __forceinline__ bool elected() {
     uint32_t r;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(r));
     return r != 0;
+}
+// One product of 16 k-values; A and B by the low words of their descriptors
+// (the high words do not change with the address). Every one elects its lane:
+// with the products in one elected branch, or with 64-bit descriptor sums, a
+// product takes 47 to 77 cycles to issue, so 40 (N = 16) or 64 (N = 128).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint32_t a_off, uint64_t b, uint32_t b_off, uint32_t idesc,
+                                       bool add) {
+    if (elected())
+        asm volatile("{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n mov.b64 a, {%1, %2};\n"
+                     " mov.b64 b, {%3, %4};\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}"
+                     ::"r"(d), "r"((uint32_t)a + a_off), "r"((uint32_t)(a >> 32)), "r"((uint32_t)b + b_off),
+                       "r"((uint32_t)(b >> 32)), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t b_off, uint32_t idesc, bool add) {
+    if (elected())
+        asm volatile("{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.u32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}"
+                     ::"r"(d), "r"(a), "r"((uint32_t)b + b_off), "r"((uint32_t)(b >> 32)), "r"(idesc),
+                       "r"((uint32_t)add) : "memory");
 }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -103,6 +112,16 @@ __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// (x, y) = (x, y) * a + b, and (x, y) += (a, b), two at a time.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {
+    asm("{\n .reg .b64 u, v, w;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %2};\n mov.b64 w, {%3, %3};\n"
+        " fma.rn.f32x2 u, u, v, w;\n mov.b64 {%0, %1}, u;\n}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+    asm("{\n .reg .b64 u, v;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n"
+        " add.rn.f32x2 u, u, v;\n mov.b64 {%0, %1}, u;\n}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
 
 // ------------------------------------------------------------------- waiting
@@ -114,6 +133,17 @@ struct Waiter {
     unsigned int* err;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
         return mbar_try_wait(bar, parity) || poll(bar, parity);
+    }
+    // For the waits between products and softmax: a waiting lane that is
+    // suspended wakes some 300 cycles after the arrival, a spinning one does not.
+    __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity) const {
+        for (int i = 0; i < 1024; ++i) {
+            uint32_t ok;
+            asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                         : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+            if (ok) return true;
+        }
+        return poll(bar, parity);
     }
     __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) const {
         const uint64_t t0 = global_ns();
@@ -128,6 +158,13 @@ struct Waiter {
         return false;
     }
 };
+
+// One arrival for the warp, after all its lanes' work (an arrival of every lane
+// is serialised: 256 of them a tile took longer than the tile).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(bar);
+}
 
 // A place in the ring of stages: consecutive uses of stage `i`, phase `ph`.
 template <int N> struct Ring {
@@ -159,19 +196,24 @@ __device__ __forceinline__ uint32_t visible(const TreeParams& p, int e, int node
 
 struct RingUse { int i; bool is_v; };  // token tile, of V or K
 
-// Four e4m3 codes -> four bf16 values (exact). A code's sign, exponent and
-// mantissa bits at their places in a bf16 are its value times 2^-120 (the
-// difference of the exponents' biases, subnormals too); the product with 2^120
-// is exact. (The conversion instructions bounded 8-bit tiles.) The NaN code
-// becomes +-480: rows that are not finite are marked by their scale.
-__device__ __forceinline__ uint32_t widen2(uint32_t x) {  // codes in the halves' high bytes
-    uint32_t r = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0x7b807b80u));
-    return r;
-}
+// Four e4m3 codes c0 .. c3 -> bf16 pairs (c0, c2) and (c1, c3), exact. A code's
+// sign, exponent and mantissa bits at their places in a bf16 are its value
+// times 2^-120 (the difference of the exponents' biases, subnormals too); the
+// product with 2^120 is exact. The even codes get there by multiplications (the
+// sign, 16 times too low then, by 240 more), the odd ones by shifts and masks:
+// the conversion instructions, and then the logic unit alone, bounded 8-bit
+// tiles. So within four channels the second and third change places, which the
+// queries and the output make good. The NaN code becomes +-480: rows that are
+// not finite are marked by their scale.
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
-    return make_uint2(widen2(__byte_perm(w, 0, 0x1404)), widen2(__byte_perm(w, 0, 0x3424)));
+    uint32_t a = (w & 0x00800080u) * 240u + (w & 0x00ff00ffu) * 16u;
+    uint32_t b = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(0x7b807b80u));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(0x7b807b80u));
+    return make_uint2(a, b);
 }
+// The channel at place c of a widened row, and the place of channel c.
+__device__ __forceinline__ constexpr int widened_channel(int c) { return (c & ~3) | (c & 1) << 1 | (c >> 1 & 1); }
 
 // V columns of fp32 values, waited for.
 template <int V> __device__ __forceinline__ void load_columns(float (&x)[V], uint32_t addr) {
@@ -317,47 +359,59 @@ __device__ __forceinline__ void copy_tiles(const TreeParams& p, const CUtensorMa
     }
 }
 
-// 256 threads widen the 8-bit tiles of NR slots into the ring's NS stages.
+// Eight warps widen the 8-bit tiles of NR slots into the ring's NS stages: four
+// of them every other tile, so that one tile's waits lie under the other's work.
+// NR is even: a slot then always is the same four's, which have seen its use
+// before (the parity they wait for would also be that of two uses before), and
+// copies may land out of order.
 template <int D, int NR, int NS>
 __device__ __forceinline__ void widen_tiles(const TreeParams& p, const uint8_t* slots, uint64_t* slot_full,
                                             uint64_t* slot_empty, uint8_t* stages, uint64_t* full, uint64_t* empty,
                                             const Waiter& wait, TreeCursor cur, long long u, long long end, int tid) {
-    constexpr int kC8 = D / 16, kMine = kT * kC8 / 256, kStep = 256 / kC8;  // 16-code chunks of a row, of a thread
-    const int c = tid % kC8, r0 = tid / kC8;
-    // the order of the two stores keeps eight lanes on different banks
-    const int odd = D == 128 ? c >> 2 : 0, at0 = tile_at(r0, 2 * c + odd), at1 = tile_at(r0, 2 * c + 1 - odd);
-    Ring<NR> raw;
-    Ring<NS> ring;
+    static_assert(NR % 2 == 0 && NS >= 2, "slots of one group");
+    constexpr int kC8 = D / 16, kMine = kT * kC8 / 128, kStep = 128 / kC8;  // 16-code chunks of a row, of a thread
+    // (the second half of a 128-channel row is another lane's of the next row:
+    // eight lanes then store to different banks)
+    const unsigned group = tid >> 7;
+    const int c = tid % kC8, r0 = ((tid & 127) / kC8) ^ (D == 128 ? c >> 2 : 0);
+    const int at0 = tile_at(r0, 2 * c), at1 = tile_at(r0, 2 * c + 1);
+    unsigned use = 0;  // of the ring, over all pieces
     TreePiece w;
     while (next_piece(p, cur, u, end, w)) {
         if (w.nodes * p.G - w.mt * p.tile_rows <= 0) continue;
-        for (int k = 2 * (w.t1 - w.t0); k > 0; --k) {
-            if (!wait(slot_full + raw.i, raw.ph)) return;
-            uint4 x[kMine];
+        for (int k = 2 * (w.t1 - w.t0); k > 0; --k, ++use) {
+            if ((use & 1) != group) continue;
+            const unsigned slot = use % NR, stage = use % NS;
+            if (!__all_sync(0xffffffffu, wait(slot_full + slot, use / NR & 1))) return;
+            const uint8_t* src = slots + slot * (kT * 128) + r0 * 128 + c * 16;
+            uint8_t* dst = stages + stage * (kT * D * 2);
+            bool stage_free = false;
 #pragma unroll
-            for (int y = 0; y < kMine; ++y)
-                x[y] = *reinterpret_cast<const uint4*>(slots + raw.i * (kT * 128) + (r0 + y * kStep) * 128 + c * 16);
-            if (!wait(empty + ring.i, ring.ph ^ 1)) return;
-            uint8_t* dst = stages + ring.i * (kT * D * 2);
+            for (int h = 0; h < kMine; h += 4) {  // (kStep is a multiple of 8: the rows' places differ by whole groups)
+                uint4 x[4];
 #pragma unroll
-            for (int y = 0; y < kMine; ++y) {  // (kStep is a multiple of 8: the rows' places differ by whole groups)
-                const uint2 a = widen4(x[y].x), b = widen4(x[y].y), d = widen4(x[y].z), f = widen4(x[y].w);
-                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, f.x, f.y);
-                *reinterpret_cast<uint4*>(dst + at0 + y * kStep * 128) = odd ? hi : lo;
-                *reinterpret_cast<uint4*>(dst + at1 + y * kStep * 128) = odd ? lo : hi;
+                for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const uint4*>(src + (h + y) * kStep * 128);
+                if (!stage_free) {
+                    if (!__all_sync(0xffffffffu, wait(empty + stage, (use / NS & 1) ^ 1))) return;
+                    stage_free = true;
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint2 a = widen4(x[y].x), b = widen4(x[y].y), d = widen4(x[y].z), f = widen4(x[y].w);
+                    *reinterpret_cast<uint4*>(dst + at0 + (h + y) * kStep * 128) = make_uint4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<uint4*>(dst + at1 + (h + y) * kStep * 128) = make_uint4(d.x, d.y, f.x, f.y);
+                }
             }
-            mbar_arrive(slot_empty + raw.i);
+            warp_arrive(slot_empty + slot);
             proxy_fence();
-            mbar_arrive(full + ring.i);
-            raw.next();
-            ring.next();
+            warp_arrive(full + stage);
         }
     }
 }
 
 // 64 threads bring a piece's queries: QR rows in blocks of at most 128, zeros
-// past its own.
-template <int D, int QR>
+// past its own; 8-bit: channels in the order of widened rows.
+template <int D, int QR, bool Q8>
 __device__ __forceinline__ void copy_queries(const TreeParams& p, uint8_t* q, uint64_t* q_full, uint64_t* q_empty,
                                              const Waiter& wait, TreeCursor cur, long long u, long long end, int tid) {
     constexpr int kChunks = D / 8, kB = QR < kT ? QR : kT;
@@ -366,7 +420,7 @@ __device__ __forceinline__ void copy_queries(const TreeParams& p, uint8_t* q, ui
     while (next_piece(p, cur, u, end, w)) {
         const int row0 = w.mt * p.tile_rows, rows = w.nodes * p.G - row0;
         if (rows <= 0) continue;
-        if (!wait(q_empty, ph)) return;
+        if (!__all_sync(0xffffffffu, wait(q_empty, ph))) return;
         ph ^= 1;
 #pragma unroll 8
         for (int x = tid; x < QR * kChunks; x += 64) {
@@ -375,10 +429,13 @@ __device__ __forceinline__ void copy_queries(const TreeParams& p, uint8_t* q, ui
             if (row < rows)
                 y = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
                                                          q_offset(p, w.e, w.h, row0 + row, D) + c * 8));
+            if constexpr (Q8)
+                y = make_uint4(__byte_perm(y.x, y.y, 0x5410), __byte_perm(y.x, y.y, 0x7632),
+                               __byte_perm(y.z, y.w, 0x5410), __byte_perm(y.z, y.w, 0x7632));
             *reinterpret_cast<uint4*>(q + (row / kB) * kB * D * 2 + tile_at(row % kB, c, kB)) = y;
         }
         proxy_fence();
-        mbar_arrive(q_full);
+        warp_arrive(q_full);
     }
 }
 

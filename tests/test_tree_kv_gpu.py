@@ -256,6 +256,33 @@ def test_offsets_past_32_bits():
     assert bool((out[:2] == 0).all())
 
 
+@pytest.mark.parametrize("kind,t,hq,hkv,d", [("e4m3", 1, 8, 8, 128), ("e4m3", 4, 32, 8, 128), ("e4m3", 12, 32, 8, 128),
+                                             ("e4m3", 40, 32, 8, 128), ("e4m3", 3, 8, 8, 64), ("bf16", 1, 8, 8, 128),
+                                             ("bf16", 7, 32, 8, 128), ("bf16", 16, 32, 8, 128), ("bf16", 64, 32, 8, 128)])
+def test_long_runs_repeat(kind, t, hq, hkv, d):
+    """Hundreds of tiles a CTA, many calls in a row: the same bits every time,
+    and no wait that gave up."""
+    b, s = 2, 100003
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((b, hkv, s + t, d), generator=gen, device="cuda") for _ in "kv")
+    ks = vs = None
+    if kind == "e4m3":
+        (k, ks), (v, vs) = quantised(k), quantised(v)
+    else:
+        k, v = k.bfloat16(), v.bfloat16()
+    q = torch.randn((b, t, hq, d), generator=gen, device="cuda").bfloat16()
+    call = ds.PreparedTreeDecode(q, k, v, s, k_scale=ks, v_scale=vs)
+    first = call().clone()
+    for _ in range(25):
+        call.out.zero_()
+        assert torch.equal(call(), first)
+    ds.check_device()
+    h = hq - 1
+    kk, vv = th.values(k[:1, -1:], None if ks is None else ks[:1, -1:]), th.values(v[:1, -1:], None if vs is None else vs[:1, -1:])
+    want, bound = th.attention(q[:1, :, h:], kk, vv, [s], [t], chain(1, t))
+    th.check(first[:1, :, h:], want, bound)
+
+
 def test_results_repeat_and_layouts_agree():
     """The same call gives the same bits, and so does the paged layout."""
     b, t, hq, hkv, d, s = 3, 9, 8, 2, 128, 1500
