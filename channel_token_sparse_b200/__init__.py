@@ -656,8 +656,9 @@ class PreparedWriteKV(_Prepared):
         elif q_out is not None or q_weight is not None:
             raise ValueError("q_out and q_weight need q")
 
-        def strided(x):
-            return (None, 0, 0) if x is None else (x.data_ptr(), x.stride(0), x.stride(1))
+        def strided(x):  # (a dimension of size 1 may have any stride: it is never taken)
+            return (None, 0, 0) if x is None else (x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0,
+                                                   x.stride(1) if x.shape[1] > 1 else 0)
 
         def ptr(x):
             return None if x is None else x.data_ptr()

@@ -14,7 +14,10 @@
 // maxima, sums and O^T, joined at the end of a piece. A tile moves a maximum
 // only when one of its scores passes it by 8 (see ds_tree_tc.cu); whether one
 // does is the only thing the four warps agree on in every tile. Sums stay a
-// thread's own until the end. Roles, ring, loaders and the treatment of values
+// thread's own until the end. Measured on a B200: one token of 32 heads over
+// 256K 8-bit tokens 521 us (65 % of the copy rate; widening the codes and the
+// issue of the products bound it), 8 nodes over 8 x 4K 8-bit 100 us, 7 nodes x
+// 4 heads over 16 x up to 8K bf16 in pages 80 us of a 93 us step. Roles, ring, loaders and the treatment of values
 // that are not finite in tree rows are those of ds_tree_tc.cu.
 #include "ds_tree_tc.cuh"
 

@@ -19,6 +19,12 @@
 // the queries. 8-bit tiles land in slots of their own and warps 12 to 19 widen
 // them to bf16 (exact) into the ring; their rows' scales multiply S and P.
 //
+// Measured on a B200: 16 nodes x 4 heads over 4 x 32K bf16 119 us (69 % of the
+// copy rate; MT = 1), 64 nodes x 4 heads over 128K bf16 220 us (625 TFLOP/s;
+// MT = 2). What bounds MT = 2 is the chain of a stream's tile: softmax (1.7K
+// cycles), PV, S and the wake-ups between them, 3.9K cycles against the 2K that
+// the products of both streams take.
+//
 // The products take every row of V with every weight, and 0 * NaN is NaN, so
 // the softmax warps tidy a tile that reaches past the prefix: rows past the
 // sequence become zeros, and the rows of tree nodes (which some query rows may

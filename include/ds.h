@@ -318,7 +318,8 @@ DS_API ds_status ds_decode_step_paged(const void* q, const void* k_pool, const v
  *     scale = max(max_c |x_c| / 448, 2^-126),   code_c = e4m3_rn(x_c / scale)
  * (IEEE divisions, round to nearest even) and stands for scale * code_c. A row
  * that holds a NaN or an infinity gets the scale NaN and reads back as NaN
- * throughout. */
+ * throughout. The NaN codes (0x7f, 0xff) occur in such rows only; under a
+ * finite scale ds_read_kv gives NaN for them and ds_tree_decode +-480. */
 
 /* Which channels of the first rot_dim rotate together, j < rot_dim / 2. */
 typedef enum {
