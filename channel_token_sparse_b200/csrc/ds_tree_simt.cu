@@ -2,11 +2,13 @@
 //
 // One pass over an item's tokens with the running maximum and sum of each
 // row's softmax: for a tile of 64 tokens the scores s = qscale * q.k (base-2
-// exponents) of 32 query rows, their new maxima, weights 2^(s - m), and the
+// exponents) of 8 to 32 query rows, their new maxima, weights 2^(s - m), and the
 // weighted values, all in fp32. A tile's K and V rows are read into
-// shared memory once and serve the 32 rows. Kept simple: fp32 caches are the
-// small and the reference ones (4 nodes over 512 tokens: 14 us, two launches'
-// latency). The CUDA cores' multiply-adds bound it from about 8 rows on.
+// shared memory once and serve the row tile. Kept simple: fp32 caches are the
+// small and the reference ones (4 nodes over 512 tokens: 12.5 us, two launches'
+// latency; 8 nodes x 4 heads over 4 x 4K 166 us against 21 us of bytes: the tile of
+// keys is read from shared memory once a row; one node x 8 heads over 2 x 16K 114 us
+// with row tiles of 8, 305 us with 32).
 #include <math.h>
 
 #include "ds_tree.cuh"
@@ -16,12 +18,15 @@ namespace ds {
 namespace {
 
 constexpr int kNT = 256;
-constexpr int kR = 32;     // query rows of a row tile
+// Query rows of a row tile: 32, or few where there are no more (a tile costs its
+// rows' arithmetic whether they exist or not; four channels a thread at least).
+constexpr int kMany = 32;
+template <int D> constexpr int kFew = D == 128 ? 8 : 16;
 constexpr int kT = 64;     // tokens of a token tile
 
-template <int D> constexpr int simt_smem() { return (kR * D + kT * (D + 4) + kT * D + kR * (kT + 4) + 3 * kR) * 4; }
+template <int D, int kR> constexpr int simt_smem() { return (kR * D + kT * (D + 4) + kT * D + kR * (kT + 4) + 3 * kR) * 4; }
 
-template <int D>
+template <int D, int kR>
 __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(16) float sm[];
     float* sq = sm;                     // [kR][D] queries, times qscale
@@ -67,17 +72,24 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const __grid_constant
         for (int tile = w.t0; tile < w.t1; ++tile) {
             const int tok0 = tile * kT;
             const int ntok = min(kT, w.prefix + w.nodes - tok0);
-            __syncthreads();
-            for (int x = tid; x < kT * D / 4; x += kNT) {
-                const int t = x / (D / 4), c = x % (D / 4) * 4;
-                float4 fk = make_float4(0.f, 0.f, 0.f, 0.f), fv = fk;
+            constexpr int kL = kT * D / 4 / kNT;  // 16-byte pieces of a thread: all read before the first is stored
+            float4 fk[kL], fv[kL];
+#pragma unroll
+            for (int j = 0; j < kL; ++j) {
+                const int x = tid + j * kNT, t = x / (D / 4), c = x % (D / 4) * 4;
+                fk[j] = fv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (t < ntok) {
                     const long long row = tree_row(p.at, w.e, w.h, tok0 + t);
-                    fk = *reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row * D + c);
-                    fv = *reinterpret_cast<const float4*>(static_cast<const float*>(p.v) + row * D + c);
+                    fk[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row * D + c);
+                    fv[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.v) + row * D + c);
                 }
-                *reinterpret_cast<float4*>(sk + t * (D + 4) + c) = fk;
-                *reinterpret_cast<float4*>(sv + t * D + c) = fv;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kL; ++j) {
+                const int x = tid + j * kNT, t = x / (D / 4), c = x % (D / 4) * 4;
+                *reinterpret_cast<float4*>(sk + t * (D + 4) + c) = fk[j];
+                *reinterpret_cast<float4*>(sv + t * D + c) = fv[j];
             }
             __syncthreads();
             // scores: a thread takes one row and tokens t = tid % 8 + 8 j
@@ -128,9 +140,7 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const __grid_constant
                 const float f = s_w[orow];
 #pragma unroll
                 for (int j = 0; j < kO; ++j) o[j] *= f;
-                for (int t = 0; t < ntok; ++t) {
-                    const float e = ss[orow * (kT + 4) + t];
-                    if (e == 0.f) continue;  // a masked token does not count, whatever its values are
+                auto add = [&](int t, float e) {
 #pragma unroll
                     for (int j = 0; j < kO / 4; ++j) {
                         const float4 v = *reinterpret_cast<const float4*>(sv + t * D + oc + 4 * kC * j);
@@ -139,6 +149,14 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const __grid_constant
                         o[4 * j + 2] = fmaf(e, v.z, o[4 * j + 2]);
                         o[4 * j + 3] = fmaf(e, v.w, o[4 * j + 3]);
                     }
+                };
+                const float* e = ss + orow * (kT + 4);
+                if (tok0 + kT <= w.prefix) {
+#pragma unroll 4
+                    for (int t = 0; t < kT; ++t) add(t, e[t]);
+                } else {
+                    for (int t = 0; t < ntok; ++t)
+                        if (e[t] != 0.f) add(t, e[t]);  // a masked token does not count, whatever its values are
                 }
             }
         }
@@ -163,25 +181,26 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const __grid_constant
     }
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t run(const TreeParams& p, cudaStream_t st) {
-    static_assert(simt_smem<D>() <= 227 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(ds_tree_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         simt_smem<D>());
+    static_assert(simt_smem<D, R>() <= 227 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(ds_tree_simt_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         simt_smem<D, R>());
     if (e != cudaSuccess) return e;
-    ds_tree_simt_kernel<D><<<p.grid, kNT, simt_smem<D>(), st>>>(p);
+    ds_tree_simt_kernel<D, R><<<p.grid, kNT, simt_smem<D, R>(), st>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 TreePlan plan_tree_simt(int rows, int d) {
-    (void)rows; (void)d;
-    return TreePlan{kR, kT, 2 * 148};
+    const int few = d == 64 ? kFew<64> : kFew<128>;
+    return TreePlan{rows <= few ? few : kMany, kT, 2 * 148};
 }
 
 cudaError_t launch_tree_simt(const TreeParams& p, int d, cudaStream_t st) {
-    return d == 64 ? run<64>(p, st) : run<128>(p, st);
+    if (p.tile_rows == kMany) return d == 64 ? run<64, kMany>(p, st) : run<128, kMany>(p, st);
+    return d == 64 ? run<64, kFew<64>>(p, st) : run<128, kFew<128>>(p, st);
 }
 
 }  // namespace ds

@@ -98,6 +98,9 @@ TREE = [
     ("f32", 2, 5, 6, 2, 128, 130, [130, 0], 0, "tree"),
     ("f32", 1, 33, 8, 1, 64, 63, None, 16, "tree"),
     ("f32", 3, 1, 2, 2, 128, 1000, [1000, 1, 0], 1, "chain"),
+    ("f32", 2, 2, 8, 2, 128, 700, None, 64, "tree"),
+    ("f32", 1, 5, 6, 2, 64, 200, None, 0, "tree"),
+    ("f32", 2, 9, 8, 2, 128, 333, [333, 64], 0, "tree"),
     ("bf16", 1, 1, 1, 1, 128, 1, None, 0, "chain"),
     ("bf16", 1, 1, 4, 4, 128, 0, None, 0, "chain"),
     ("bf16", 2, 16, 8, 2, 128, 777, None, 0, "tree"),
