@@ -17,8 +17,6 @@
 
 namespace ds {
 
-constexpr int kTreeMaxGrid = 2 * 148;  // CTAs of a launch, at most (two a B200 SM)
-
 struct TreeParams {
     const void *q, *k, *v;
     const float *k_scale, *v_scale;
@@ -181,11 +179,6 @@ __device__ __forceinline__ float* part_of(const TreeParams& p, int cta, int begi
     return p.part + ((size_t)cta * 2 + begins) * ((size_t)p.part_rows * (d + 2));
 }
 
-// Whether row tile position r of piece w is a query row of a node that exists.
-__device__ __forceinline__ bool row_exists(const TreeParams& p, const TreePiece& w, int r) {
-    const int row = w.mt * p.tile_rows + r;
-    return row < w.nodes * p.G;
-}
 // Element offset of query row `row` of (entry, kv head) in q and out.
 __device__ __forceinline__ size_t q_offset(const TreeParams& p, int e, int h, int row, int d) {
     const int node = row / p.G, g = row - node * p.G;

@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
         uint32_t p_ph[2] = {0, 0}, q_ph = 0;
         constexpr uint32_t kS = instr_desc(N, false, false), kO = instr_desc(N, true, true);
         const uint32_t q_addr = smem_u32(smem), p_addr = smem_u32(smem + C::oP), st_addr = smem_u32(smem + C::oStage);
-        auto all_spin = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait.spin(bar, parity)) != 0; };
         while (warp == 8) {
             const bool more = next_piece(p, cur, u, end, w);
             if (!__any_sync(0xffffffffu, more)) break;
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
             for (int i = -2; ok && i < n; ++i) {
                 const int s = i & 1;
                 if (i + 2 < n) {
-                    ok = all_spin(full + ring.i, ring.ph);
+                    ok = all_wait(full + ring.i, ring.ph);
                     if (!ok) break;
                     const int b = 2 * s + (((i + 2) >> 1) & 1);
                     const uint32_t d = tm + b * N;
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                     ring.next();
                 }
                 if (i >= 0) {
-                    ok = all_spin(full + ring.i, ring.ph) && all_spin(p_full + s, p_ph[s]);
+                    ok = all_wait(full + ring.i, ring.ph) && all_wait(p_full + s, p_ph[s]);
                     if (!ok) break;
                     p_ph[s] ^= 1;
                     tc_fence_after();
@@ -292,7 +291,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                     }
                 }
                 const int buf = (i >> 1) & 1;
-                fine = __all_sync(0xffffffffu, wait.spin(s_full + 2 * st + buf, s_ph[buf])) && fine;
+                fine = all_wait(s_full + 2 * st + buf, s_ph[buf]) && fine;
                 s_ph[buf] ^= 1;
                 if (masked && !C::kQ8) {
                     // The V stage is tidied (see ds_tree_tc.cu). Only now: while S^T was not

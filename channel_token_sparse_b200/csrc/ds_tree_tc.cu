@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
         const uint32_t q_addr = smem_u32(smem), st_addr = smem_u32(smem + C::oStage);
         auto s_of = [&](int s) { return tm + s * kT; };
         auto o_of = [&](int s) { return tm + 2 * kT + s * D; };
-        auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait.spin(bar, parity)) != 0; };
+        auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         auto ready = [&](const Ring<NS>& r) { return all_wait(full + r.i, r.ph); };
         auto commit = [&](uint64_t* bar) { if (elected()) tc_commit(bar); };
         auto scores = [&](int s, int stage) {  // S = Q K^T of stream s
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                     }
                     __syncwarp();
                 }
-                ok = __all_sync(0xffffffffu, wait.spin(s_full + st, s_ph));
+                ok = all_wait(s_full + st, s_ph);
                 if (!ok) break;
                 s_ph ^= 1;
                 if (masked && !C::kQ8) {

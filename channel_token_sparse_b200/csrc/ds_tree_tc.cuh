@@ -31,11 +31,6 @@ __device__ __forceinline__ void tc_ld(uint32_t (&r)[8], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tc_st(uint32_t addr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                   : "memory");
-}
 __device__ __forceinline__ void tc_ld(uint32_t (&r)[16], uint32_t addr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
                  "%13,%14,%15}, [%16];"
@@ -133,17 +128,6 @@ struct Waiter {
     unsigned int* err;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
         return mbar_try_wait(bar, parity) || poll(bar, parity);
-    }
-    // For the waits between products and softmax: a waiting lane that is
-    // suspended wakes some 300 cycles after the arrival, a spinning one does not.
-    __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity) const {
-        for (int i = 0; i < 1024; ++i) {
-            uint32_t ok;
-            asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-                         : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-            if (ok) return true;
-        }
-        return poll(bar, parity);
     }
     __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) const {
         const uint64_t t0 = global_ns();
