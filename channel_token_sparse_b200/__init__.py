@@ -566,26 +566,56 @@ def _on_one_device(*ts):
 class _Prepared:
     """A C-ABI call with its arguments checked and converted once. Calling it
     enqueues the call on `stream`, or on the stream that is current on the
-    tensors' device at that time, and returns the outputs."""
+    tensors' device at that time, and returns the outputs.
+
+    A handle may be called on one stream after another and dropped at any time:
+    its tensors' memory is not given out again before what it enqueued is done.
+    Its calls share its outputs and workspace, so two of them must not run at
+    the same time: one that follows on another stream waits for the one before
+    (an event), and streams that run side by side have a handle each. A graph
+    that captured a call needs the handle for as long as it is replayed."""
 
     def _bind(self, fn, args, dev, stream, keep, result):
         self._fn, self._args, self._dev, self._stream = fn, args, dev, stream
         self._keep = keep  # keeps the memory alive
         self._result = result
+        # streams that the tensors' memory waits for when it is freed: the one it belongs to
+        self._streams = {_torch().cuda.current_stream(dev).cuda_stream} if stream is None else set()
+
+    def _record(self, stream):
+        """The allocator hears of a stream that the tensors were not made on."""
+        torch = _torch()
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return  # nothing runs now, and replays are the graph's owner's to order
+        for x in _tensors(self._keep, self._result):
+            x.record_stream(stream)
+        self._streams.add(stream.cuda_stream)
 
     def __call__(self):
         torch = _torch()
-        dev, stream = self._dev, self._stream
+        dev = self._dev
+        stream = torch.cuda.current_stream(dev) if self._stream is None else self._stream
+        s = stream.cuda_stream
+        if s not in self._streams:
+            self._record(stream)
         if torch.cuda.current_device() != dev.index:
             with torch.cuda.device(dev):
-                s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
                 st = self._fn(*self._args, s)
         else:
-            s = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
             st = self._fn(*self._args, s)
         if st != DS_OK:
             raise DSError(st, last_error())
         return self._result
+
+
+def _tensors(*xs):
+    """The tensors among xs and in their tuples."""
+    for x in xs:
+        if isinstance(x, tuple):
+            yield from _tensors(*x)
+        elif x is not None:
+            yield x
 
 
 def _alloc(shape, dtype, dev, stream):
@@ -734,7 +764,7 @@ def read_kv(k, v, k_scale, v_scale, s: int, seq_lens=None, block_table=None, dty
         fn = lib().ds_read_kv_paged
         args = [ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), ptr(block_table), block_table.shape[1], k.shape[2],
                 k.shape[0], ptr(seq_lens), b, hkv, int(s), d, *tail]
-    call._bind(fn, args, dev, stream, None, (k_out, v_out))
+    call._bind(fn, args, dev, stream, (k, v, k_scale, v_scale, seq_lens, block_table), (k_out, v_out))
     return call()
 
 
@@ -769,8 +799,9 @@ def tree_decode_workspace(b, t, hq, hkv, s, d, kv_dtype=DS_BF16) -> int:
 
 class PreparedTreeDecode(_Prepared):
     """tree_decode bound once, with its output and workspace; calling it
-    enqueues the attention and returns out. set_length(s) moves to another
-    prefix length, up to the one it was made with."""
+    enqueues the attention and returns out. Two calls of one handle must not
+    run at the same time: they share both. set_length(s) moves to another prefix
+    length, up to the one it was made with."""
 
     _S_ARG = {False: 13, True: 17}
 
