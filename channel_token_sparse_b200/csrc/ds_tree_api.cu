@@ -21,6 +21,13 @@ ds_status launched(cudaError_t e, const char* what) {
     DS_FAIL(DS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Whether a * b * c rows (a, b >= 1) of d channels reach 2^40 elements. The
+// products of two sizes fit 64 bits, those of three do not.
+bool too_large(long long a, long long b, long long c, int d) {
+    const long long most = ((1ll << 40) - 1) / d;
+    return a * b > most || c > most / (a * b);
+}
+
 struct Pool {
     const int32_t* table = nullptr;
     int max_blocks = 0, page_size = 0, num_blocks = 0;
@@ -31,7 +38,7 @@ ds_status cache_rows(const Pool* pool, int b, int hkv, int s_cap, int d, CacheRo
     at->hkv = hkv;
     if (!pool) {
         if (s_cap < 1) DS_FAIL(DS_ERR_INVALID_ARG, "s_cap (%d) must be >= 1", s_cap);
-        if ((long long)b * hkv * s_cap >= (1ll << 40) / d) DS_FAIL(DS_ERR_UNSUPPORTED, "cache too large");
+        if (too_large(b, hkv, s_cap, d)) DS_FAIL(DS_ERR_UNSUPPORTED, "cache too large");
         at->s_cap = s_cap;
         *rows = s_cap;
         return DS_OK;
@@ -44,7 +51,7 @@ ds_status cache_rows(const Pool* pool, int b, int hkv, int s_cap, int d, CacheRo
         DS_FAIL(DS_ERR_INVALID_ARG, "page_size %d must be a power of two in [1, 65536]", pool->page_size);
     if (pool->num_blocks < 1 || pool->max_blocks < 1)
         DS_FAIL(DS_ERR_INVALID_ARG, "num_blocks and max_blocks must be >= 1");
-    if (((long long)pool->num_blocks * hkv << shift) >= (1ll << 40) / d) DS_FAIL(DS_ERR_UNSUPPORTED, "pool too large");
+    if (too_large(pool->num_blocks, hkv, 1 << shift, d)) DS_FAIL(DS_ERR_UNSUPPORTED, "pool too large");
     const long long r = (long long)pool->max_blocks << shift;
     at->block_table = pool->table;
     at->max_blocks = pool->max_blocks;
@@ -124,7 +131,7 @@ ds_status read_kv(const void* k, const void* v, const float* k_scale, const floa
     if ((r = cache_rows(pool, b, hkv, s_cap, d, &a.at, &rows)) != DS_OK) return r;
     if (s < 0 || s > rows || s > s_out_cap)
         DS_FAIL(DS_ERR_INVALID_ARG, "need 0 <= s (%d) <= cache rows (%d) and s_out_cap (%d)", s, rows, s_out_cap);
-    if ((long long)b * hkv * s_out_cap >= (1ll << 40) / d) DS_FAIL(DS_ERR_UNSUPPORTED, "output too large");
+    if (too_large(b, hkv, s_out_cap, d)) DS_FAIL(DS_ERR_UNSUPPORTED, "output too large");
     if (s == 0) return DS_OK;
     a.k = k; a.v = v; a.k_scale = k_scale; a.v_scale = v_scale; a.seq_lens = seq_lens;
     a.b = b; a.hkv = hkv; a.s = s; a.d = d; a.k_out = k_out; a.v_out = v_out;

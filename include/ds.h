@@ -354,8 +354,8 @@ typedef enum {
  *   k_cache, v_cache  dtype cache_dt: dt, or DS_E4M3 with k_scale and v_scale
  * Two tokens of one call that go to the same row leave either's contents.
  * inv_freq, positions, starts, lens and the scales need 4-byte alignment, the
- * other pointers 16. DS_ERR_UNSUPPORTED for b * t > 2^30 or a cache dtype that
- * is neither. */
+ * other pointers 16. DS_ERR_UNSUPPORTED for b * t > 2^30, more than 2^20 heads of
+ * a kind, a cache of 2^40 elements or more, or a cache dtype that is neither. */
 DS_API ds_status ds_write_kv(const void* q, long long q_bs, long long q_ts,
                              const void* k, long long k_bs, long long k_ts,
                              const void* v, long long v_bs, long long v_ts, ds_dtype dt,
@@ -385,7 +385,8 @@ DS_API ds_status ds_write_kv_paged(const void* q, long long q_bs, long long q_ts
  * layout that ds_build_label_cache and the decode calls read. seq_lens [b]
  * (int32, clamped into [0, s]; or NULL) gives each entry's own row count; rows
  * past it, and rows past s, are not touched. The v triple (v_cache, v_scale,
- * v_out) may be NULL together: only the keys are read then. */
+ * v_out) may be NULL together: only the keys are read then.
+ * DS_ERR_UNSUPPORTED for a cache or an output of 2^40 elements or more. */
 DS_API ds_status ds_read_kv(const void* k_cache, const void* v_cache, const float* k_scale,
                             const float* v_scale, const int32_t* seq_lens, int b, int hkv, int s,
                             int s_cap, int d, void* k_out, void* v_out, ds_dtype out_dt,
@@ -418,6 +419,8 @@ DS_API ds_status ds_read_kv_paged(const void* k_pool, const void* v_pool, const 
  *              [0, t]; or NULL (t). Nodes past it are seen by none, and their
  *              rows of out are not touched.
  *   s          0 <= s, s + t <= s_cap;  1 <= t <= 256
+ *   b, hkv     b * hkv <= 2^26 and hq / hkv <= 8; the cache (the whole pool)
+ *              below 2^31 - 256 rows (DS_ERR_UNSUPPORTED beyond)
  *   sm_scale   <= 0 selects 1/sqrt(d)
  *   ws         device scratch of ds_tree_decode_workspace_size() bytes, 16-byte
  *              aligned, whose contents on entry do not matter. Calls that may
