@@ -274,9 +274,13 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                 if constexpr (C::kQ8) {
                     ks = sc_k * p.qscale;
                     vs = sc_v;
-                    if (node_t >= 0 && !(isfinite(ks) && isfinite(vs))) {  // not seen by all rows: set aside
-                        ks = vs = 0.f;
-                        atomicOr(bad + (node_t >> 5), 1u << (node_t & 31));
+                    if (!(isfinite(ks) && isfinite(vs))) {
+                        if (node_t < 0) {  // an infinite key scale makes the scores NaN
+                            ks = fmaf(ks, 0.f, ks);
+                        } else {  // not seen by all rows: set aside
+                            ks = vs = 0.f;
+                            atomicOr(bad + (node_t >> 5), 1u << (node_t & 31));
+                        }
                     }
                 }
                 bool fine = true;

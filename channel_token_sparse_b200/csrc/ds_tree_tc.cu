@@ -304,9 +304,13 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                     for (int k = 0; k < kT / 32; ++k) {
                         const int j = tok0 + k * 32 + lane - w.prefix;
                         float a = sc_k[k] * p.qscale, b = sc_v[k];
-                        if (j >= 0 && !(isfinite(a) && isfinite(b))) {  // a tree row, not seen by all: set aside
-                            a = b = 0.f;
-                            atomicOr(bad + (j >> 5), 1u << (j & 31));
+                        if (!(isfinite(a) && isfinite(b))) {
+                            if (j < 0) {  // an infinite key scale makes the scores NaN
+                                a = fmaf(a, 0.f, a);
+                            } else {  // not seen by all rows: set aside
+                                a = b = 0.f;
+                                atomicOr(bad + (j >> 5), 1u << (j & 31));
+                            }
                         }
                         ks[k * 32 + lane] = a;
                         vs[k * 32 + lane] = b;

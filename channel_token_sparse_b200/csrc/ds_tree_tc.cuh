@@ -241,7 +241,8 @@ __device__ __forceinline__ void tidy_values(uint8_t* v, int b, int have, int nod
     }
 }
 // What the marked nodes that `node` sees add to channel c: the sum of their
-// values that are not finite (8-bit: NaN, for a row whose scales are not).
+// values that are not finite (8-bit: of a row whose scales are not; NaN where
+// that is the key's).
 template <int TYPE, int D>
 __device__ __forceinline__ float not_finite_seen(const TreeParams& p, const TreePiece& w, int node, const uint32_t* bad, int c) {
     float sum = 0.f;
@@ -250,7 +251,10 @@ __device__ __forceinline__ float not_finite_seen(const TreeParams& p, const Tree
         for (uint32_t see = bad[q] & mask_word(p, w.e, node, q); see; see &= see - 1) {
             const long long row = tree_row(p.at, w.e, w.h, w.prefix + 32 * q + __ffs(see) - 1);
             if constexpr (TYPE == kTreeE4M3) {
-                if (!isfinite(p.k_scale[row] * p.qscale) || !isfinite(p.v_scale[row])) sum = NAN;
+                uint32_t h;  // two halves; the lower one is the code's value
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)static_cast<const uint8_t*>(p.v)[row * D + c]));
+                sum += __half2float(__ushort_as_half((uint16_t)h)) * p.v_scale[row];
+                if (!isfinite(p.k_scale[row] * p.qscale)) sum = NAN;
             } else {
                 const float f = Elem<bf16_t>::to_f32(static_cast<const bf16_t*>(p.v)[row * D + c]);
                 if (!isfinite(f)) sum += f;

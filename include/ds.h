@@ -318,8 +318,10 @@ DS_API ds_status ds_decode_step_paged(const void* q, const void* k_pool, const v
  *     scale = max(max_c |x_c| / 448, 2^-126),   code_c = e4m3_rn(x_c / scale)
  * (IEEE divisions, round to nearest even) and stands for scale * code_c. A row
  * that holds a NaN or an infinity gets the scale NaN and reads back as NaN
- * throughout. The NaN codes (0x7f, 0xff) occur in such rows only; under a
- * finite scale ds_read_kv gives NaN for them and ds_tree_decode +-480. */
+ * throughout. An infinite scale, which no row written here has, gives infinite
+ * values (NaN for the code 0), and NaN scores where it is a key's. The NaN codes
+ * (0x7f, 0xff) may stand in rows of a NaN scale only: under another scale
+ * ds_read_kv gives NaN for them and ds_tree_decode +-480. */
 
 /* Which channels of the first rot_dim rotate together, j < rot_dim / 2. */
 typedef enum {

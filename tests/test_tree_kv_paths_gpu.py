@@ -49,3 +49,46 @@ def test_dropped_handle_keeps_its_memory_until_another_stream_is_done():
     assert all(x.data_ptr() + size <= at or at + size <= x.data_ptr() for x in new)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# query rows a kv head (t * hq / hkv) that reach each kernel of 16-bit and 8-bit caches: the two of up
+# to 32 rows, one row block, two, and two in several row tiles
+ROWS = {"16": (4, 4), "32": (7, 4), "128": (24, 4), "256": (50, 4), "1024": (128, 8)}
+
+
+@pytest.mark.parametrize("rows", list(ROWS))
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("where", ["key", "value"])
+def test_infinite_scales(rows, d, where):
+    """An infinite scale of a prefix row, then of a tree row: a key's makes the
+    scores of the nodes that see it NaN, a value's their outputs infinite (NaN
+    where the code is 0). Nodes that do not see the tree row keep their bits."""
+    t, g = ROWS[rows]
+    b, hkv, s, inf = 1, 2, 300, float("inf")
+    gen = torch.Generator().manual_seed(41)
+    k, v, ks, vs = caches(gen, "e4m3", b, hkv, s + t, d)
+    k.view(torch.uint8)[0, :, 37, 0], v.view(torch.uint8)[0, :, 37, 0] = 0x38, 0
+    q = randn(gen, b, t, g * hkv, d).bfloat16().cuda()
+    see = torch.eye(t, dtype=torch.bool).repeat(b, 1, 1)
+    see[:, :, 1] = torch.arange(t) % 3 == 1
+    mask = th.bits_of(see).cuda()
+    kd, vd, ksd, vsd = cu(k, v, ks, vs)
+
+    def run():
+        return ds.tree_decode(q, kd, vd, s, mask=mask, k_scale=ksd, v_scale=vsd).cpu()
+
+    plain = run()
+    assert bool(torch.isfinite(plain).all())
+    scale = ksd if where == "key" else vsd
+    keep = scale.clone()
+    for row in (37, s + 1):
+        scale.copy_(keep)
+        scale[:, :, row] = inf
+        got = run()
+        seen = torch.ones(t, dtype=torch.bool) if row == 37 else see[0, :, 1]
+        assert torch.equal(got[:, ~seen], plain[:, ~seen])
+        if where == "key":
+            assert bool(got[:, seen].isnan().all())
+            continue
+        want = (v[0, :, row].float() * inf).repeat_interleave(g, 0).expand(int(seen.sum()), -1, -1)
+        assert torch.equal(got[0, seen].nan_to_num(7.0), want.nan_to_num(7.0))
