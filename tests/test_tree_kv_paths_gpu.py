@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import channel_token_sparse_b200 as ds  # noqa: E402
-from test_tree_kv_gpu import caches, cu, randn  # noqa: E402
+from test_tree_kv_gpu import caches, chain, cu, paged, randn  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -92,3 +92,111 @@ def test_infinite_scales(rows, d, where):
             continue
         want = (v[0, :, row].float() * inf).repeat_interleave(g, 0).expand(int(seen.sum()), -1, -1)
         assert torch.equal(got[0, seen].nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+def _not_finite(kind, rows, d, what, page=0):
+    """Many short items, so that a CTA goes from items with rows that are not
+    finite to items without: clean caches and the same ones with such rows."""
+    t, g = ROWS[rows]
+    hkv = 8 if t * g <= 32 else 4
+    b, s = (24 if t * g <= 128 else 12), 150
+    gen = torch.Generator().manual_seed(43)
+    lens = [(37 * e) % (s + 1) for e in range(b)]
+    nodes = [(t, max(t - 1, 0), min(t, 3), t, 0, t)[e % 6] for e in range(b)]
+    k, v, ks, vs = caches(gen, kind, b, hkv, s + t + 5, d)
+    q = randn(gen, b, t, g * hkv, d).to(torch.float32 if kind == "f32" else torch.bfloat16)
+    see = torch.rand((b, t, t), generator=gen) < 0.4
+    i = torch.arange(t)
+    see[:, :, 1], see[:, :, 2] = i % 4 == 1, i % 3 == 2
+    clean = [None if x is None else x.clone() for x in (k, v, ks, vs)]
+    nan = float("nan")
+    for e in range(b):
+        behind = slice(lens[e] + nodes[e], None)
+        if kind == "e4m3":
+            for c, sc in ((k, ks), (v, vs)):
+                c.view(torch.uint8)[e, :, behind], sc[e, :, behind] = 0x7f, what
+        else:
+            k[e, :, behind], v[e, :, behind] = what, what
+        if e % 2 == 1 and nodes[e] > 2:  # a key
+            if kind == "e4m3":
+                ks[e, :, lens[e] + 2] = nan
+            else:
+                k[e, :, lens[e] + 2, 5] = nan
+        if e % 3 == 0 and nodes[e] > 1:  # a value
+            if kind == "e4m3":
+                vs[e, :, lens[e] + 1] = what
+            else:
+                v[e, :, lens[e] + 1, 3::8] = what
+    lens_d, nodes_d = (torch.tensor(x, dtype=torch.int32).cuda() for x in (lens, nodes))
+    outs = []
+    for c in (clean, (k, v, ks, vs)):
+        out = torch.full(q.shape, 7.0, device="cuda")
+        kw = dict(mask=th.bits_of(see).cuda(), seq_lens=lens_d, node_lens=nodes_d, out=out)
+        if page:
+            pools, table = paged(c, page, torch.Generator().manual_seed(1))
+            kd, vd, ksd, vsd = cu(*pools)
+            ds.tree_decode_paged(q.cuda(), kd, vd, table.cuda(), s, k_scale=ksd, v_scale=vsd, **kw)
+        else:
+            kd, vd, ksd, vsd = cu(*c)
+            ds.tree_decode(q.cuda(), kd, vd, s, k_scale=ksd, v_scale=vsd, **kw)
+        outs.append(out.cpu())
+    return q, clean, v, lens, nodes, see, g, outs
+
+
+@pytest.mark.parametrize("kind,rows,d,page", [
+    *[(kind, rows, d, 0) for kind in ("bf16", "e4m3") for rows in ROWS for d in (64, 128)],
+    *[(kind, rows, 128, page) for kind in ("bf16", "e4m3") for rows, page in (("16", 16), ("128", 1), ("256", 64))],
+    ("f32", "16", 128, 0), ("f32", "16", 64, 0), ("f32", "128", 128, 16), ("f32", "256", 64, 0)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_rows_that_are_not_finite_in_every_kernel(kind, rows, d, page, what):
+    """A node that does not see a row which is not finite keeps its bits, one
+    that sees it gets what the formula gives, and rows past an entry's own nodes
+    stay as they were."""
+    q, clean, v, lens, nodes, see, g, (plain, got) = _not_finite(kind, rows, d, what, page)
+    b, t = q.shape[:2]
+    i = torch.arange(t)
+    want = plain.clone()
+    assert bool(torch.isfinite(plain).all())
+    for e in range(b):
+        n = nodes[e]
+        assert bool((plain[e, n:] == 7.0).all())
+        if e % 3 == 0 and n > 1:
+            at = torch.nonzero(see[e, :n, 1] & (i[:n] >= 0)).flatten()
+            if kind == "e4m3":
+                x = v[e, :, lens[e] + 1].float() * what
+                want[e, at] = x.repeat_interleave(g, 0)
+            else:
+                want[e, at, :, 3::8] = what
+        if e % 2 == 1 and n > 2:
+            want[e, torch.nonzero(see[e, :n, 2]).flatten()] = float("nan")
+    # an infinite weight sum cannot be: infinities of one value row keep their sign
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(5.0, 1e30, -1e30), want.nan_to_num(5.0, 1e30, -1e30))
+    # the clean call itself, for the first kv head of the first entries
+    k0, v0 = (th.values(c[:6, :1], None if sc is None else sc[:6, :1]) for c, sc in ((clean[0], clean[2]), (clean[1], clean[3])))
+    ref, bound = th.attention(q[:6, :, :1], k0, v0, lens[:6], nodes[:6], see, sloppy=kind != "f32")
+    for e in range(6):
+        ref[e, nodes[e]:], bound[e, nodes[e]:] = 7.0, 0.0
+    th.check(plain[:6, :, :1], ref, bound)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+def test_node_counts_that_leave_row_tiles_empty(kind):
+    """The widest tree (256 nodes of 8 heads: eight row tiles or more), whose
+    entries have all, few or none of the nodes."""
+    b, t, hkv, g, d, s = 3, 256, 1, 8, 64, 200
+    gen = torch.Generator().manual_seed(47)
+    lens, nodes = [200, 0, 77], [256, 3, 0]
+    k, v, ks, vs = caches(gen, kind, b, hkv, s + t, d)
+    q = randn(gen, b, t, g, d).to(torch.float32 if kind == "f32" else torch.bfloat16)
+    kd, vd, ksd, vsd = cu(k, v, ks, vs)
+    lens_d, nodes_d = (torch.tensor(x, dtype=torch.int32).cuda() for x in (lens, nodes))
+    out = torch.full(q.shape, 7.0, device="cuda")
+    ds.tree_decode(q.cuda(), kd, vd, s, seq_lens=lens_d, node_lens=nodes_d, k_scale=ksd, v_scale=vsd, out=out)
+    h = [0, 7]
+    want, bound = th.attention(q[:, :, h], th.values(k, ks), th.values(v, vs), lens, nodes, chain(b, t),
+                               sloppy=kind != "f32")
+    for e in range(b):
+        want[e, nodes[e]:], bound[e, nodes[e]:] = 7.0, 0.0
+        assert bool((out[e, nodes[e]:] == 7.0).all())
+    th.check(out[:, :, h], want, bound)
