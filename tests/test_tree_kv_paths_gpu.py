@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import channel_token_sparse_b200 as ds  # noqa: E402
-from test_tree_kv_gpu import caches, chain, cu, paged, randn  # noqa: E402
+from test_tree_kv_gpu import caches, chain, cu, paged, quantised, randn  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -200,3 +200,79 @@ def test_node_counts_that_leave_row_tiles_empty(kind):
         want[e, nodes[e]:], bound[e, nodes[e]:] = 7.0, 0.0
         assert bool((out[e, nodes[e]:] == 7.0).all())
     th.check(out[:, :, h], want, bound)
+
+
+@pytest.mark.parametrize("starts", [None, [0, 70001, 123456789]])
+@pytest.mark.parametrize("page", [0, 8])
+def test_rotation_by_the_rows_themselves(starts, page):
+    """Without positions a token's position is its cache row (far ones lie
+    outside the cache: their queries turn all the same)."""
+    b, t, hq, hkv, d, cap = 3, 9, 4, 2, 64, 24
+    gen = torch.Generator().manual_seed(53)
+    x = randn(gen, b, t, hq + 2 * hkv, d)
+    inv = torch.pow(torch.tensor(10000.0, dtype=torch.float64), -2.0 * torch.arange(d // 2) / d).float()
+    pos = (torch.tensor(starts or [0] * b)[:, None] + torch.arange(t)).to(torch.int32)
+    shape, table = ((b, hkv, cap, d), None) if not page else ((9, hkv, page, d), torch.randperm(9, generator=gen).view(3, 3))
+    kc, vc, _, _ = ds.new_kv_cache(shape, torch.float32)
+    xd = x.cuda()
+    got = ds.write_kv(xd[:, :, :hq], xd[:, :, hq:hq + hkv], xd[:, :, hq + hkv:], kc, vc, inv_freq=inv.cuda(),
+                      starts=None if starts is None else torch.tensor(starts, dtype=torch.int32).cuda(),
+                      block_table=None if table is None else table.to(torch.int32).cuda())
+    want, norms = th.heads(x[:, :, :hq], None, 0.0, pos, inv, False)
+    th.check(got, want, th.HALF[torch.float32] * want.abs() + th.STEPS * norms, "q")
+    want, norms = th.heads(x[:, :, hq:hq + hkv], None, 0.0, pos, inv, False)
+    kk, vv = (th.gather(c, table) if page else c.cpu() for c in (kc, vc))
+    for e in range(b):
+        if int(pos[e, 0]) < cap:
+            th.check(kk[e, :, :t], want[e].transpose(0, 1), (th.HALF[torch.float32] * want[e].abs() + th.STEPS * norms[e]).transpose(0, 1), "k")
+            assert torch.equal(vv[e, :, :t], x[e, :, hq + hkv:].transpose(0, 1))
+            assert bool((kk[e, :, t:] == 0).all()) and bool((vv[e, :, t:] == 0).all())
+        else:
+            assert bool((kk[e] == 0).all()) and bool((vv[e] == 0).all())
+
+
+def _room(n):
+    if torch.cuda.mem_get_info()[0] < n << 30:
+        pytest.skip(f"needs {n} GB of device memory")
+
+
+@pytest.mark.parametrize("page", [0, 1 << 16])
+def test_writes_past_32_bits(page):
+    """A cache of more than 2^32 elements: rows at its end, and no other."""
+    b, hkv, d, t = 3, 8, 128, 2
+    cap = 1 << 21
+    _room(60)
+    shape = (b, hkv, cap, d) if not page else (b * (cap // page), hkv, page, d)
+    kc, vc, ks, vs = ds.new_kv_cache(shape, th.E4M3)
+    gen = torch.Generator().manual_seed(59)
+    x = randn(gen, b, t, 2 * hkv, d).bfloat16().cuda()
+    table = torch.arange(b * (cap // page), dtype=torch.int32).view(b, -1).cuda() if page else None
+    starts = torch.tensor([5, cap, cap - t], dtype=torch.int32).cuda()
+    ds.write_kv(None, x[:, :, :hkv], x[:, :, hkv:], kc, vc, starts=starts, k_scale=ks, v_scale=vs, block_table=table)
+    for c, sc, first in ((kc, ks, 0), (vc, vs, hkv)):
+        for e, row in ((0, 5), (2, cap - t)):
+            at = (e, slice(None), slice(row, row + t)) if not page else (
+                e * (cap // page) + row // page, slice(None), slice(row % page, row % page + t))
+            y = x[e, :, first:first + hkv].float().transpose(0, 1).cpu()
+            codes, scale = quantised(y)
+            assert torch.equal(sc[at].cpu(), scale)
+            assert torch.equal(c[at].cpu().view(torch.uint8), codes.view(torch.uint8))
+            sc[at] = 0
+        assert not bool(sc.any())
+
+
+def test_reads_past_32_bits():
+    """A cache and outputs of more than 2^32 elements: the last entry's rows."""
+    b, hkv, d, s = 3, 8, 128, 1 << 21
+    _room(60)
+    kc, vc, ks, vs = ds.new_kv_cache((b, hkv, s, d), th.E4M3)
+    gen = torch.Generator().manual_seed(61)
+    k, v, k_scale, v_scale = caches(gen, "e4m3", 1, hkv, 50, d)
+    for c, x in ((kc, k), (vc, v)):
+        c.view(torch.uint8)[2, :, -50:] = x[0].view(torch.uint8).cuda()
+    ks[2, :, -50:], vs[2, :, -50:] = k_scale[0].cuda(), v_scale[0].cuda()
+    outs = [torch.empty((b, hkv, s, d), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    ds.read_kv(kc, vc, ks, vs, s, k_out=outs[0], v_out=outs[1])
+    for o, x, sc in ((outs[0], k, k_scale), (outs[1], v, v_scale)):
+        assert torch.equal(o[2, :, -50:].cpu(), (x[0].float() * sc[0, :, :, None]).bfloat16())
+        assert not bool(o[2, :, -60:-50].any()) and not bool(o[0, 0, :1000].any())
