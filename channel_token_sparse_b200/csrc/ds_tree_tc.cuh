@@ -122,20 +122,24 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
 // ------------------------------------------------------------------- waiting
 
 // A wait gives up after about a second, or when another one of the CTA did:
-// every role then leaves its loop (see mbar_wait_bounded).
+// every role then leaves its loop (see mbar_wait_bounded). That is far more than
+// a tile takes. The wait for a whole piece (2^24 tiles at most) has a limit of
+// ten minutes: whatever a piece could hang on is waited for by another role,
+// whose second ends this wait too.
+constexpr uint64_t kTileWait = 1000000000ull, kPieceWait = 600 * kTileWait;
 struct Waiter {
     volatile int* stop;
     unsigned int* err;
-    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-        return mbar_try_wait(bar, parity) || poll(bar, parity);
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, uint64_t limit = kTileWait) const {
+        return mbar_try_wait(bar, parity) || poll(bar, parity, limit);
     }
-    __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) const {
+    __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity, uint64_t limit) const {
         const uint64_t t0 = global_ns();
         for (;;) {
             for (int i = 0; i < 64; ++i)
                 if (mbar_try_wait(bar, parity)) return true;
             if (*stop) return false;
-            if (global_ns() - t0 > 1000000000ull) break;
+            if (global_ns() - t0 > limit) break;
         }
         *stop = 1;
         note_timeout(err, 3);
@@ -408,7 +412,7 @@ __device__ __forceinline__ void copy_queries(const TreeParams& p, uint8_t* q, ui
     while (next_piece(p, cur, u, end, w)) {
         const int row0 = w.mt * p.tile_rows, rows = w.nodes * p.G - row0;
         if (rows <= 0) continue;
-        if (!__all_sync(0xffffffffu, wait(q_empty, ph))) return;
+        if (!__all_sync(0xffffffffu, wait(q_empty, ph, kPieceWait))) return;
         ph ^= 1;
 #pragma unroll 8
         for (int x = tid; x < QR * kChunks; x += 64) {
