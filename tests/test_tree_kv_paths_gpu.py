@@ -276,3 +276,21 @@ def test_reads_past_32_bits():
     for o, x, sc in ((outs[0], k, k_scale), (outs[1], v, v_scale)):
         assert torch.equal(o[2, :, -50:].cpu(), (x[0].float() * sc[0, :, :, None]).bfloat16())
         assert not bool(o[2, :, -60:-50].any()) and not bool(o[0, 0, :1000].any())
+
+
+def test_pieces_of_more_than_a_second():
+    """So long a context that one CTA's piece of an item takes longer than a
+    wait for a tile may: 105M tokens (all pages of the prefix are one block)
+    under 2048 query rows."""
+    page, blocks, t, g, d, b = 1 << 16, 1600, 256, 8, 64, 19
+    gen = torch.Generator(device="cuda").manual_seed(67)
+    k, v = (torch.randn((1, 1, page, d), generator=gen, device="cuda").bfloat16() for _ in "kv")
+    q = torch.randn((b, t, g, d), generator=gen, device="cuda").bfloat16()
+    table = torch.zeros((b, blocks), dtype=torch.int32, device="cuda")
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    out = ds.tree_decode_paged(q, k, v, table, blocks * page - t)
+    end.record()
+    ds.check_device()  # no wait gave up
+    assert start.elapsed_time(end) > 1500.0
+    assert bool(torch.isfinite(out).all())
