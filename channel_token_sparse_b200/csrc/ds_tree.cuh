@@ -33,6 +33,7 @@ struct TreeParams {
     void* out;
     int out_bf16;
     float* part;     // partial results: see part_of
+    float* sums;     // second accumulators of ds_tree_tc.cu, where pieces may be long; or NULL
     int part_rows;   // rows of a partial: min(rows, tile_rows), rounded up to a multiple of 4
     unsigned int* err;
 };
@@ -201,6 +202,9 @@ __device__ __forceinline__ long long tree_row(const CacheRows& c, int e, int h, 
     return (((long long)blk * c.hkv + h) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
 }
 
+// Token tiles of a stream between two moves of its tensor-core sums (ds_tree_tc.cuh).
+constexpr int kTreeSpan = 128;
+
 enum TreeType { kTreeF32 = 0, kTreeBF16 = 1, kTreeE4M3 = 2 };
 
 // Launches. f32 (ds_tree_simt.cu):
@@ -209,6 +213,8 @@ TreePlan plan_tree_simt(int rows, int d);
 cudaError_t launch_tree_simt(const TreeParams& p, int d, cudaStream_t st);
 // bf16 and e4m3 (ds_tree_tc.cu; up to 32 query rows: ds_tree_few.cu).
 TreePlan plan_tree_tc(int rows, int d);
+// Bytes of their second accumulators, for pieces of at most `tiles` token tiles.
+size_t tree_tc_sums(const TreePlan& plan, int grid, long long tiles, int d);
 cudaError_t launch_tree_tc(const TreeParams& p, int type, int d, cudaStream_t st);
 cudaError_t launch_tree_combine(const TreeParams& p, int d, cudaStream_t st);
 

@@ -139,7 +139,7 @@ ds_status read_kv(const void* k, const void* v, const float* k_scale, const floa
     return launched(ds::launch_read_kv(a, stream), "cache read launch");
 }
 
-struct TreeShape { int type; ds::TreePlan plan; int grid, n_mt, part_rows; size_t ws; };
+struct TreeShape { int type; ds::TreePlan plan; int grid, n_mt, part_rows; size_t parts, ws; };
 
 ds_status tree_shape(int b, int t, int hq, int hkv, int s, int d, ds_dtype kvdt, TreeShape* o) {
     ds_status r = check_heads(b, hq, hkv, d);
@@ -159,10 +159,15 @@ ds_status tree_shape(int b, int t, int hq, int hkv, int s, int d, ds_dtype kvdt,
     o->n_mt = (rows + o->plan.tile_rows - 1) / o->plan.tile_rows;
     // a multiple of 4 keeps every place, and the values behind its rows' statistics, 16-byte aligned
     o->part_rows = ((rows < o->plan.tile_rows ? rows : o->plan.tile_rows) + 3) / 4 * 4;
-    const long long units = (long long)b * hkv * o->n_mt * (((long long)s + t + o->plan.tile_tokens - 1) / o->plan.tile_tokens);
+    const long long tiles = ((long long)s + t + o->plan.tile_tokens - 1) / o->plan.tile_tokens;
+    const long long units = (long long)b * hkv * o->n_mt * tiles;
     o->grid = units < o->plan.grid ? (int)units : o->plan.grid;
     // two places a CTA for pieces of split items
-    o->ws = (size_t)o->grid * 2 * o->part_rows * (d + 2) * 4;
+    o->ws = o->parts = (size_t)o->grid * 2 * o->part_rows * (d + 2) * 4;
+    if (o->type != ds::kTreeF32) {  // a piece has an item's tiles at most, and a CTA's share of all
+        const long long share = (units + o->grid - 1) / o->grid;
+        o->ws += ds::tree_tc_sums(o->plan, o->grid, tiles < share ? tiles : share, d);
+    }
     return DS_OK;
 }
 
@@ -200,6 +205,7 @@ ds_status tree_decode(const void* q, const void* k, const void* v, ds_dtype kvdt
     p.qscale = (sm_scale > 0.f ? sm_scale : 1.0f / sqrtf((float)d)) * 1.4426950408889634f;
     p.out = out; p.out_bf16 = out_dt == DS_BF16;
     p.part = static_cast<float*>(ws);
+    p.sums = sh.ws > sh.parts ? p.part + sh.parts / 4 : nullptr;
     cudaError_t e = ds::device_status_word(&p.err);
     if (e != cudaSuccess) return launched(e, "cudaGetSymbolAddress");
     e = sh.type == ds::kTreeF32 ? ds::launch_tree_simt(p, d, stream) : ds::launch_tree_tc(p, sh.type, d, stream);

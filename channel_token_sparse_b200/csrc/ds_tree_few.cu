@@ -40,14 +40,15 @@ struct Cfg {
     static constexpr int kRaw = kQ8 ? 4 : 0, kRawBytes = kT * 128;  // slots of 8-bit tiles
     static constexpr int kQ = N * D * 2, kP = kT * 128;  // P^T: a token's weights in 128 bytes
     static constexpr int oP = kQ, oStage = oP + 2 * kP, oRaw = oStage + kStages * kStage, oStat = oRaw + kRaw * kRawBytes;
-    static constexpr int kStat = 16 * N;  // floats: maxima [2][N], factors [2][N], partial [2][4][N], result [4][N]
+    // floats: maxima [2][N], factors [2][N], partial [2][4][N], result [4][N], maxima of the second O^T [2][N]
+    static constexpr int kStat = 18 * N;
     static constexpr int oBar = oStat + kStat * 4;
     static constexpr int kBars = 2 * kStages + 2 * kRaw + 12;
     static constexpr int kSmem = oBar + kBars * 8 + 64;
     static_assert(kSmem <= 227 * 1024 && kQ % 1024 == 0, "shared memory");
     // K_i and V_i are five uses of the ring apart at most: see the tidying
     static_assert(kQ8 || kStages >= 5, "stages");
-    static constexpr int kCols = N == 32 ? 256 : 128;  // tensor memory: 4 S^T, 2 O^T of N columns
+    static constexpr int kCols = N == 32 ? 256 : 128;  // tensor memory: 4 S^T, 2 O^T and 2 second O^T of N columns
 };
 
 // K0 K1, then K_{i+2} V_i.
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
     float* s_fac = s_max + 2 * N;                              // [2][N]
     float* s_red = s_fac + 2 * N;                              // [2][4][N]
     float* s_fin = s_red + 8 * N;                              // [4][N]: factors of the two streams, 1 / sum, -
+    float* s_last = s_fin + 4 * N;                             // [2][N]
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::oBar);
     uint64_t* empty = full + NS;
     uint64_t* s_full = empty + NS;   // [2][2] S^T of a stream's tile is there
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                     const uint64_t va = smem_desc(st_addr + ring.i * C::kStage, D == 128 ? kT * 128 : 0, 1024);
                     const uint64_t pb = smem_desc(p_addr + s * C::kP, 16, 1024);
 #pragma unroll
-                    for (int k = 0; k < kT / 16; ++k) mma_ss(d, va, k * 128, pb, k * 128, kO, i >= 2 || k > 0);
+                    for (int k = 0; k < kT / 16; ++k) mma_ss(d, va, k * 128, pb, k * 128, kO, (i >> 1) % kSpan > 0 || k > 0);
                     if (elected()) {
                         tc_commit(o_done + s);
                         tc_commit(empty + ring.i);
@@ -244,6 +246,26 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
         const int t = threadIdx.x & 127;                // token of a tile; channel of O^T
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + 2 * st * N, t_o = tmem + lanes + 4 * N;
+        // Moves O^T into the second one (back: the other way), with the second one before
+        // where there is one (see kSpan). That is relative to the maxima of the move before.
+        auto move_sums = [&](bool both, bool back) {
+            const float *m = s_max + st * N, *last = s_last + st * N;
+            const uint32_t o = t_o + st * N, second = o + 2 * N;
+#pragma unroll 1
+            for (int c0 = 0; c0 < N; c0 += 16) {
+                float a[16], b[16];
+                load_columns<16>(a, o + c0);
+                if (both) {
+                    load_columns<16>(b, second + c0);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) a[c] = fmaf(b[c], ex2(last[c0 + c] - m[c0 + c]), a[c]);
+                }
+                store_columns<16>((back ? o : second) + c0, a);
+            }
+            tc_wait_st();
+            group_sync(bar);
+            if (t < N) s_last[st * N + t] = m[t];
+        };
         uint8_t* pt = smem + C::oP + st * C::kP + t * 128;
         // a wait that the warpgroup leaves with one answer, so that none of its warps waits for one that left
         auto group_wait = [&](uint64_t* b, uint32_t parity) { return !any_of_group(bar, !wait(b, parity)); };
@@ -267,136 +289,144 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
                 sc_v = there ? __ldg(p.v_scale + row) : 0.f;
             };
             if (C::kQ8 && st < n) scales((w.t0 + st) * kT + t);
-            for (int i = st; i < n; i += 2) {
-                const int tok0 = (w.t0 + i) * kT, node_t = tok0 + t - w.prefix;  // this token's node (negative: prefix)
-                const bool masked = tok0 + kT > w.prefix;
-                float ks = p.qscale, vs = 1.f;
-                if constexpr (C::kQ8) {
-                    ks = sc_k * p.qscale;
-                    vs = sc_v;
-                    if (!(isfinite(ks) && isfinite(vs))) {
-                        if (node_t < 0) {  // an infinite key scale makes the scores NaN
-                            ks = fmaf(ks, 0.f, ks);
-                        } else {  // not seen by all rows: set aside
-                            ks = vs = 0.f;
-                            atomicOr(bad + (node_t >> 5), 1u << (node_t & 31));
+            for (int i = st; ok && i < n;) {
+                for (const int span = min(n, i + 2 * kSpan); i < span; i += 2) {
+                    const int tok0 = (w.t0 + i) * kT, node_t = tok0 + t - w.prefix;  // this token's node (negative: prefix)
+                    const bool masked = tok0 + kT > w.prefix;
+                    float ks = p.qscale, vs = 1.f;
+                    if constexpr (C::kQ8) {
+                        ks = sc_k * p.qscale;
+                        vs = sc_v;
+                        if (!(isfinite(ks) && isfinite(vs))) {
+                            if (node_t < 0) {  // an infinite key scale makes the scores NaN
+                                ks = fmaf(ks, 0.f, ks);
+                            } else {  // not seen by all rows: set aside
+                                ks = vs = 0.f;
+                                atomicOr(bad + (node_t >> 5), 1u << (node_t & 31));
+                            }
                         }
                     }
-                }
-                bool fine = true;
-                uint32_t vis = ~0u;  // query rows that see this token
-                if (masked) {
-                    if (node_t >= w.nodes) vis = 0;
-                    else if (node_t >= 0) {
-                        vis = 0;
-                        const uint32_t g = (1u << p.G) - 1;
-                        for (int r = 0, x = row0 / p.G; r < rows; ++x, r += p.G)
-                            if (mask_word(p, w.e, x, node_t >> 5) >> (node_t & 31) & 1) vis |= g << r;
-                    }
-                }
-                const int buf = (i >> 1) & 1;
-                fine = all_wait(s_full + 2 * st + buf, s_ph[buf]) && fine;
-                s_ph[buf] ^= 1;
-                if (masked && !C::kQ8) {
-                    // The V stage is tidied (see ds_tree_tc.cu). Only now: while S^T was not
-                    // there, the stage's use before could still be landing, and the parity
-                    // of this one's phase would be that of two before.
-                    const unsigned use = uses + FewOrder::v_use(i, n), stage = use % NS;
-                    fine = all_wait(full + stage, use / NS & 1) && fine;
-                    if (fine)
-                        tidy_values<D>(smem + C::oStage + stage * C::kStage, max(w.prefix - tok0, 0),
-                                       min(tokens - tok0, kT), tok0 - w.prefix, bad, t);
-                }
-                if (done > 0) fine = all_wait(o_done + st, (o_cnt - 1) & 1) && fine;  // P^T and O^T are free
-                tc_fence_after();
-                float x[HN];
-                auto scores = [&](int h) {
-                    load_columns<HN>(x, t_s + buf * N + h * HN);
-#pragma unroll
-                    for (int c = 0; c < HN; ++c) x[c] *= ks;
+                    bool fine = true;
+                    uint32_t vis = ~0u;  // query rows that see this token
                     if (masked) {
-#pragma unroll
-                        for (int c = 0; c < HN; ++c) x[c] = (vis >> (h * HN + c) & 1) ? x[c] : -INFINITY;
-                    }
-                };
-                bool move = done == 0 || !fine;
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    scores(h);
-                    if (done > 0) {
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int c = 0; c < HN; c += 4) {
-                            const float4 m4 = *reinterpret_cast<const float4*>(mx + h * HN + c);
-                            top = fmaxf(fmaxf(top, x[c] - m4.x), x[c + 1] - m4.y);
-                            top = fmaxf(fmaxf(top, x[c + 2] - m4.z), x[c + 3] - m4.w);
+                        if (node_t >= w.nodes) vis = 0;
+                        else if (node_t >= 0) {
+                            vis = 0;
+                            const uint32_t g = (1u << p.G) - 1;
+                            for (int r = 0, x = row0 / p.G; r < rows; ++x, r += p.G)
+                                if (mask_word(p, w.e, x, node_t >> 5) >> (node_t & 31) & 1) vis |= g << r;
                         }
-                        move = move || top > 8.f;
                     }
-                }
-                if (any_of_group(bar, move)) {
-                    if (any_of_group(bar, !fine)) { ok = false; break; }
-                    // the tile's maxima, over 32 tokens and then over the four warps
+                    const int buf = (i >> 1) & 1;
+                    fine = all_wait(s_full + 2 * st + buf, s_ph[buf]) && fine;
+                    s_ph[buf] ^= 1;
+                    if (masked && !C::kQ8) {
+                        // The V stage is tidied (see ds_tree_tc.cu). Only now: while S^T was not
+                        // there, the stage's use before could still be landing, and the parity
+                        // of this one's phase would be that of two before.
+                        const unsigned use = uses + FewOrder::v_use(i, n), stage = use % NS;
+                        fine = all_wait(full + stage, use / NS & 1) && fine;
+                        if (fine)
+                            tidy_values<D>(smem + C::oStage + stage * C::kStage, max(w.prefix - tok0, 0),
+                                           min(tokens - tok0, kT), tok0 - w.prefix, bad, t);
+                    }
+                    if (done > 0) fine = all_wait(o_done + st, (o_cnt - 1) & 1) && fine;  // P^T and O^T are free
+                    tc_fence_after();
+                    float x[HN];
+                    auto scores = [&](int h) {
+                        load_columns<HN>(x, t_s + buf * N + h * HN);
+#pragma unroll
+                        for (int c = 0; c < HN; ++c) x[c] *= ks;
+                        if (masked) {
+#pragma unroll
+                            for (int c = 0; c < HN; ++c) x[c] = (vis >> (h * HN + c) & 1) ? x[c] : -INFINITY;
+                        }
+                    };
+                    bool move = done == 0 || !fine;
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        scores(h);
+                        if (done > 0) {
+                            float top = -INFINITY;
+#pragma unroll
+                            for (int c = 0; c < HN; c += 4) {
+                                const float4 m4 = *reinterpret_cast<const float4*>(mx + h * HN + c);
+                                top = fmaxf(fmaxf(top, x[c] - m4.x), x[c + 1] - m4.y);
+                                top = fmaxf(fmaxf(top, x[c + 2] - m4.z), x[c + 3] - m4.w);
+                            }
+                            move = move || top > 8.f;
+                        }
+                    }
+                    if (any_of_group(bar, move)) {
+                        if (any_of_group(bar, !fine)) { ok = false; break; }
+                        // the tile's maxima, over 32 tokens and then over the four warps
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            if (H > 1) scores(h);
+                            float y[HN];
+#pragma unroll
+                            for (int c = 0; c < HN; ++c) y[c] = x[c];
+                            const float top = warp_reduce_to_lane<HN, true>(y);
+                            if (lane % (32 / HN) == 0) red[(warp & 3) * N + h * HN + lane / (32 / HN)] = top;
+                        }
+                        group_sync(bar);
+                        if (t < N) {
+                            const float top = fmaxf(fmaxf(red[t], red[N + t]), fmaxf(red[2 * N + t], red[3 * N + t]));
+                            const float old = done > 0 ? mx[t] : kFloor;
+                            const float now = done == 0 || top > old + 8.f ? fmaxf(top, old) : old;
+                            fac[t] = ex2(old - now);
+                            mx[t] = now;
+                        }
+                        group_sync(bar);
+                        if (done > 0) {
+#pragma unroll
+                            for (int h = 0; h < H; ++h) {
+                                float y[HN];
+                                load_columns<HN>(y, t_o + st * N + h * HN);
+#pragma unroll
+                                for (int c = 0; c < HN; ++c) {
+                                    const float f = fac[h * HN + c];
+                                    y[c] *= f;
+                                    l[h * HN + c] *= f;
+                                }
+                                store_columns<HN>(t_o + st * N + h * HN, y);
+                            }
+                            tc_wait_st();
+                        }
+                    }
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         if (H > 1) scores(h);
-                        float y[HN];
 #pragma unroll
-                        for (int c = 0; c < HN; ++c) y[c] = x[c];
-                        const float top = warp_reduce_to_lane<HN, true>(y);
-                        if (lane % (32 / HN) == 0) red[(warp & 3) * N + h * HN + lane / (32 / HN)] = top;
-                    }
-                    group_sync(bar);
-                    if (t < N) {
-                        const float top = fmaxf(fmaxf(red[t], red[N + t]), fmaxf(red[2 * N + t], red[3 * N + t]));
-                        const float old = done > 0 ? mx[t] : kFloor;
-                        const float now = done == 0 || top > old + 8.f ? fmaxf(top, old) : old;
-                        fac[t] = ex2(old - now);
-                        mx[t] = now;
-                    }
-                    group_sync(bar);
-                    if (done > 0) {
+                        for (int c = 0; c < HN; c += 8) {
+                            const float4 a = *reinterpret_cast<const float4*>(mx + h * HN + c);
+                            const float4 b = *reinterpret_cast<const float4*>(mx + h * HN + c + 4);
+                            float e[8] = {x[c] - a.x, x[c + 1] - a.y, x[c + 2] - a.z, x[c + 3] - a.w,
+                                          x[c + 4] - b.x, x[c + 5] - b.y, x[c + 6] - b.z, x[c + 7] - b.w};
 #pragma unroll
-                        for (int h = 0; h < H; ++h) {
-                            float y[HN];
-                            load_columns<HN>(y, t_o + st * N + h * HN);
-#pragma unroll
-                            for (int c = 0; c < HN; ++c) {
-                                const float f = fac[h * HN + c];
-                                y[c] *= f;
-                                l[h * HN + c] *= f;
+                            for (int k = 0; k < 8; ++k) {
+                                e[k] = ex2(e[k]);
+                                l[h * HN + c + k] += e[k];
+                                if constexpr (C::kQ8) e[k] *= vs;
                             }
-                            store_columns<HN>(t_o + st * N + h * HN, y);
+                            const uint4 y = make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
+                                                       pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
+                            *reinterpret_cast<uint4*>(pt + ((((h * HN + c) >> 3) ^ (t & 7)) << 4)) = y;
                         }
-                        tc_wait_st();
                     }
+                    proxy_fence();
+                    tc_fence_before();
+                    warp_arrive(p_full + st);
+                    if (C::kQ8 && i + 2 < n) scales(tok0 + 2 * kT + t);  // (before, the fence would wait for them)
+                    ++o_cnt;
+                    ++done;
                 }
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    if (H > 1) scores(h);
-#pragma unroll
-                    for (int c = 0; c < HN; c += 8) {
-                        const float4 a = *reinterpret_cast<const float4*>(mx + h * HN + c);
-                        const float4 b = *reinterpret_cast<const float4*>(mx + h * HN + c + 4);
-                        float e[8] = {x[c] - a.x, x[c + 1] - a.y, x[c + 2] - a.z, x[c + 3] - a.w,
-                                      x[c + 4] - b.x, x[c + 5] - b.y, x[c + 6] - b.z, x[c + 7] - b.w};
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            e[k] = ex2(e[k]);
-                            l[h * HN + c + k] += e[k];
-                            if constexpr (C::kQ8) e[k] *= vs;
-                        }
-                        const uint4 y = make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
-                                                   pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
-                        *reinterpret_cast<uint4*>(pt + ((((h * HN + c) >> 3) ^ (t & 7)) << 4)) = y;
-                    }
+                if (ok && i < n) {  // O^T starts again
+                    ok = group_wait(o_done + st, (o_cnt - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    move_sums(done > kSpan, false);
                 }
-                proxy_fence();
-                tc_fence_before();
-                warp_arrive(p_full + st);
-                if (C::kQ8 && i + 2 < n) scales(tok0 + 2 * kT + t);  // (before, the fence would wait for them)
-                ++o_cnt;
-                ++done;
             }
             if (!ok) break;
             uses += 2 * n;
@@ -404,6 +434,10 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, N>::kThreads, 1) ds_tree_few_kern
             if (done > 0) {
                 ok = group_wait(o_done + st, (o_cnt - 1) & 1);
                 if (!ok) break;
+                if (done > kSpan) {
+                    tc_fence_after();
+                    move_sums(true, true);
+                }
             }
 #pragma unroll
             for (int h = 0; h < H; ++h) {

@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                     if (ok && i >= 0) {
                         ok = weights(i & 1);
                         if (!ok) break;
-                        values(i & 1, rv.i, i >= 2);
+                        values(i & 1, rv.i, (i >> 1) % kSpan > 0);
                         commit(empty + rv.i);
                     }
                     if (ok && i + 2 < n) {
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                         if (i >= 0) {
                             ok = weights(s);
                             if (!ok) break;
-                            values(s, rv.i, i > 0);
+                            values(s, rv.i, i % kSpan > 0);
                         }
                         if (more) scores(s, ring.i);
                     }
@@ -267,9 +267,38 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
         float* ks = reinterpret_cast<float*>(smem + C::oScale) + warp * 2 * kT;
         float* vs = ks + kT;
         uint32_t s_ph = 0, o_cnt = 0, x_ph = 0;     // o_cnt: products awaited or due on o_done
-        Ring<NS> vring;                             // the V stages, for the looks at tree rows
         unsigned uses = 0;                          // ring uses of the pieces before
         bool ok = true;
+        // This row's second sums (see kSpan), in the workspace: four channels of 128 rows
+        // side by side. They are relative to the maximum of their last addition, which
+        // stands in ml until the piece's end.
+        float4* sums = reinterpret_cast<float4*>(p.sums) + ((size_t)blockIdx.x * 2 + st) * (kT * D / 4) + r;
+        auto add_sums = [&](float m, bool both, bool back) {  // the sums (or, back, O) = O (+ the sums)
+            const float last = ml[st * kT + r], f = both && last != -INFINITY ? ex2(last - m) : 0.f;
+            if (!back) ml[st * kT + r] = m;
+#pragma unroll 1
+            for (int k = 0; k < D / 32; ++k) {
+                uint32_t y[32];
+                tc_ld(y, t_o + st * D + 32 * k);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    float4* at = sums + (8 * k + j / 4) * kT;
+                    float4 o = make_float4(__uint_as_float(y[j]), __uint_as_float(y[j + 1]), __uint_as_float(y[j + 2]),
+                                           __uint_as_float(y[j + 3]));
+                    if (both) {
+                        const float4 b = *at;
+                        o.x = fmaf(b.x, f, o.x); o.y = fmaf(b.y, f, o.y);
+                        o.z = fmaf(b.z, f, o.z); o.w = fmaf(b.w, f, o.w);
+                    }
+                    if (!back) *at = o;
+                    y[j] = __float_as_uint(o.x); y[j + 1] = __float_as_uint(o.y);
+                    y[j + 2] = __float_as_uint(o.z); y[j + 3] = __float_as_uint(o.w);
+                }
+                if (back) tc_st(t_o + st * D + 32 * k, y);
+            }
+            if (back) tc_wait_st();
+        };
         while (ok && next_piece(p, cur, u, end, w)) {
             const int row0 = w.mt * p.tile_rows, rows = w.nodes * p.G - row0;
             if (rows <= 0) continue;
@@ -295,168 +324,176 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                 }
             };
             if (C::kQ8 && i0 < n) scales((w.t0 + i0) * kT);
-            for (int i = i0; i < n; i += kEvery) {
-                const int tok0 = (w.t0 + i) * kT;
-                const bool masked = tok0 + kT > w.prefix;
-                if constexpr (C::kQ8) {  // the tile's scales; those of the stream's next tile are read meanwhile
-                    __syncwarp();
+            for (int i = i0; ok && i < n;) {
+                for (const int span = min(n, i + kEvery * kSpan); i < span; i += kEvery) {
+                    const int tok0 = (w.t0 + i) * kT;
+                    const bool masked = tok0 + kT > w.prefix;
+                    if constexpr (C::kQ8) {  // the tile's scales; those of the stream's next tile are read meanwhile
+                        __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < kT / 32; ++k) {
-                        const int j = tok0 + k * 32 + lane - w.prefix;
-                        float a = sc_k[k] * p.qscale, b = sc_v[k];
-                        if (!(isfinite(a) && isfinite(b))) {
-                            if (j < 0) {  // an infinite key scale makes the scores NaN
-                                a = fmaf(a, 0.f, a);
-                            } else {  // not seen by all rows: set aside
-                                a = b = 0.f;
-                                atomicOr(bad + (j >> 5), 1u << (j & 31));
-                            }
-                        }
-                        ks[k * 32 + lane] = a;
-                        vs[k * 32 + lane] = b;
-                    }
-                    __syncwarp();
-                }
-                ok = all_wait(s_full + st, s_ph);
-                if (!ok) break;
-                s_ph ^= 1;
-                if (masked && !C::kQ8) {
-                    // The V stage is tidied before the products read it (see the top). Only now:
-                    // while S was not there, the stage's use before could still be landing, and
-                    // the parity of this one's phase would be that of two before.
-                    const unsigned use = uses + TcOrder<MT>::v_use(i, n), stage = use % NS;
-                    ok = all_wait(full + stage, use / NS & 1);
-                    if (!ok) break;
-                    tidy_values<D>(smem + C::oStage + stage * C::kStage, max(w.prefix - tok0, 0), min(tokens - tok0, kT),
-                                   tok0 - w.prefix, bad, threadIdx.x & 127);
-                    proxy_fence();
-                }
-                tc_fence_after();
-                if (warp_live) {
-                    if (masked) {  // what a row does not see gets the score -infinity
-#pragma unroll 1
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t vis = live ? visible(p, w.e, node, w.nodes, tok0 + 32 * k - w.prefix) : 0u;
-                            uint32_t x[32];
-                            tc_ld(x, t_s + 32 * k);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                float f = __uint_as_float(x[j]);
-                                if constexpr (C::kQ8) f *= ks[32 * k + j];
-                                x[j] = (vis >> j & 1) ? __float_as_uint(f) : 0xff800000u;
-                            }
-                            tc_st(t_s + 32 * k, x);
-                        }
-                        tc_wait_st();
-                        if constexpr (C::kQ8) {  // the scales are in these scores
-                            __syncwarp();
-                            for (int k = lane; k < kT; k += 32) ks[k] = 1.f;
-                            __syncwarp();
-                        }
-                    }
-                    // The tile's maximum. MT = 2, where the softmax is on the critical path:
-                    // the scores stay in registers from here on (64 nodes over 128K: 217 ->
-                    // 210 us; one row block is 6 % slower so); else they are read once more.
-                    constexpr int kHeld = C::kQ8 || MT == 1 ? 2 : 4;
-                    uint32_t x[kHeld][32];
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int k = 0; k < 4; k += kHeld) {
-#pragma unroll
-                        for (int h = 0; h < kHeld; ++h) tc_ld(x[h], t_s + 32 * (k + h));
-                        tc_wait_ld();
-                        float a[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int h = 0; h < kHeld; ++h) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                float f[8];
-#pragma unroll
-                                for (int q = 0; q < 8; ++q) f[q] = __uint_as_float(x[h][j + q]);
-                                if constexpr (C::kQ8) {
-                                    const float4 s0 = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j);
-                                    const float4 s1 = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j + 4);
-                                    f[0] *= s0.x; f[1] *= s0.y; f[2] *= s0.z; f[3] *= s0.w;
-                                    f[4] *= s1.x; f[5] *= s1.y; f[6] *= s1.z; f[7] *= s1.w;
+                        for (int k = 0; k < kT / 32; ++k) {
+                            const int j = tok0 + k * 32 + lane - w.prefix;
+                            float a = sc_k[k] * p.qscale, b = sc_v[k];
+                            if (!(isfinite(a) && isfinite(b))) {
+                                if (j < 0) {  // an infinite key scale makes the scores NaN
+                                    a = fmaf(a, 0.f, a);
+                                } else {  // not seen by all rows: set aside
+                                    a = b = 0.f;
+                                    atomicOr(bad + (j >> 5), 1u << (j & 31));
                                 }
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) a[q] = fmaxf(fmaxf(a[q], f[2 * q]), f[2 * q + 1]);
                             }
+                            ks[k * 32 + lane] = a;
+                            vs[k * 32 + lane] = b;
                         }
-                        mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+                        __syncwarp();
                     }
-                    if constexpr (!C::kQ8) mx *= p.qscale;
-                    if (done == 0) {
-                        m = mx;
-                    } else {
-                        const bool move = mx > m + 8.f;
-                        if (__any_sync(0xffffffffu, move)) {
-                            // the products of this stream before are done; nothing else touches O
-                            ok = all_wait(o_done + st, (o_cnt - 1) & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const float f = move ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
-                            if (move) m = mx;
-                            l *= f;
-#pragma unroll
-                            for (int k = 0; k < D / 32; ++k) {
-                                uint32_t y[32];
-                                tc_ld(y, t_o + st * D + 32 * k);
+                    ok = all_wait(s_full + st, s_ph);
+                    if (!ok) break;
+                    s_ph ^= 1;
+                    if (masked && !C::kQ8) {
+                        // The V stage is tidied before the products read it (see the top). Only now:
+                        // while S was not there, the stage's use before could still be landing, and
+                        // the parity of this one's phase would be that of two before.
+                        const unsigned use = uses + TcOrder<MT>::v_use(i, n), stage = use % NS;
+                        ok = all_wait(full + stage, use / NS & 1);
+                        if (!ok) break;
+                        tidy_values<D>(smem + C::oStage + stage * C::kStage, max(w.prefix - tok0, 0), min(tokens - tok0, kT),
+                                       tok0 - w.prefix, bad, threadIdx.x & 127);
+                        proxy_fence();
+                    }
+                    tc_fence_after();
+                    if (warp_live) {
+                        if (masked) {  // what a row does not see gets the score -infinity
+#pragma unroll 1
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t vis = live ? visible(p, w.e, node, w.nodes, tok0 + 32 * k - w.prefix) : 0u;
+                                uint32_t x[32];
+                                tc_ld(x, t_s + 32 * k);
                                 tc_wait_ld();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                                tc_st(t_o + st * D + 32 * k, y);
+                                for (int j = 0; j < 32; ++j) {
+                                    float f = __uint_as_float(x[j]);
+                                    if constexpr (C::kQ8) f *= ks[32 * k + j];
+                                    x[j] = (vis >> j & 1) ? __float_as_uint(f) : 0xff800000u;
+                                }
+                                tc_st(t_s + 32 * k, x);
+                            }
+                            tc_wait_st();
+                            if constexpr (C::kQ8) {  // the scales are in these scores
+                                __syncwarp();
+                                for (int k = lane; k < kT; k += 32) ks[k] = 1.f;
+                                __syncwarp();
                             }
                         }
-                    }
-                    const float base = m == -INFINITY ? 0.f : -m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        // The tile's maximum. MT = 2, where the softmax is on the critical path:
+                        // the scores stay in registers from here on (64 nodes over 128K: 217 ->
+                        // 210 us; one row block is 6 % slower so); else they are read once more.
+                        constexpr int kHeld = C::kQ8 || MT == 1 ? 2 : 4;
+                        uint32_t x[kHeld][32];
+                        float mx = -INFINITY;
 #pragma unroll 1
-                    for (int k = 0; k < 4; k += kHeld) {
-                        if constexpr (kHeld < 4) {
+                        for (int k = 0; k < 4; k += kHeld) {
 #pragma unroll
                             for (int h = 0; h < kHeld; ++h) tc_ld(x[h], t_s + 32 * (k + h));
                             tc_wait_ld();
-                        }
+                            float a[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int h = 0; h < kHeld; ++h) {
-                            uint32_t y[16];
+                            for (int h = 0; h < kHeld; ++h) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                float f[4];
+                                for (int j = 0; j < 32; j += 8) {
+                                    float f[8];
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) f[q] = __uint_as_float(x[h][j + q]);
-                                if constexpr (C::kQ8) {
-                                    const float4 sc = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j);
-                                    f[0] = fmaf(f[0], sc.x, base); f[1] = fmaf(f[1], sc.y, base);
-                                    f[2] = fmaf(f[2], sc.z, base); f[3] = fmaf(f[3], sc.w, base);
-                                } else {
-                                    fma2(f[0], f[1], p.qscale, base);
-                                    fma2(f[2], f[3], p.qscale, base);
+                                    for (int q = 0; q < 8; ++q) f[q] = __uint_as_float(x[h][j + q]);
+                                    if constexpr (C::kQ8) {
+                                        const float4 s0 = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j);
+                                        const float4 s1 = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j + 4);
+                                        f[0] *= s0.x; f[1] *= s0.y; f[2] *= s0.z; f[3] *= s0.w;
+                                        f[4] *= s1.x; f[5] *= s1.y; f[6] *= s1.z; f[7] *= s1.w;
+                                    }
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) a[q] = fmaxf(fmaxf(a[q], f[2 * q]), f[2 * q + 1]);
                                 }
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) f[q] = ex2(f[q]);
-                                add2(sum[0], sum[1], f[0], f[1]);
-                                add2(sum[2], sum[3], f[2], f[3]);
-                                if constexpr (C::kQ8) {
-                                    const float4 sc = *reinterpret_cast<const float4*>(vs + 32 * (k + h) + j);
-                                    f[0] *= sc.x; f[1] *= sc.y; f[2] *= sc.z; f[3] *= sc.w;
-                                }
-                                y[j / 2] = pack_bf16x2(f[0], f[1]);
-                                y[j / 2 + 1] = pack_bf16x2(f[2], f[3]);
                             }
-                            tc_st(t_s + 16 * (k + h), y);
+                            mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                         }
+                        if constexpr (!C::kQ8) mx *= p.qscale;
+                        if (done == 0) {
+                            m = mx;
+                        } else {
+                            const bool move = mx > m + 8.f;
+                            if (__any_sync(0xffffffffu, move)) {
+                                // the products of this stream before are done; nothing else touches O
+                                ok = all_wait(o_done + st, (o_cnt - 1) & 1);
+                                if (!ok) break;
+                                tc_fence_after();
+                                const float f = move ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
+                                if (move) m = mx;
+                                l *= f;
+#pragma unroll
+                                for (int k = 0; k < D / 32; ++k) {
+                                    uint32_t y[32];
+                                    tc_ld(y, t_o + st * D + 32 * k);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                                    tc_st(t_o + st * D + 32 * k, y);
+                                }
+                            }
+                        }
+                        const float base = m == -INFINITY ? 0.f : -m;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                        for (int k = 0; k < 4; k += kHeld) {
+                            if constexpr (kHeld < 4) {
+#pragma unroll
+                                for (int h = 0; h < kHeld; ++h) tc_ld(x[h], t_s + 32 * (k + h));
+                                tc_wait_ld();
+                            }
+#pragma unroll
+                            for (int h = 0; h < kHeld; ++h) {
+                                uint32_t y[16];
+#pragma unroll
+                                for (int j = 0; j < 32; j += 4) {
+                                    float f[4];
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) f[q] = __uint_as_float(x[h][j + q]);
+                                    if constexpr (C::kQ8) {
+                                        const float4 sc = *reinterpret_cast<const float4*>(ks + 32 * (k + h) + j);
+                                        f[0] = fmaf(f[0], sc.x, base); f[1] = fmaf(f[1], sc.y, base);
+                                        f[2] = fmaf(f[2], sc.z, base); f[3] = fmaf(f[3], sc.w, base);
+                                    } else {
+                                        fma2(f[0], f[1], p.qscale, base);
+                                        fma2(f[2], f[3], p.qscale, base);
+                                    }
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) f[q] = ex2(f[q]);
+                                    add2(sum[0], sum[1], f[0], f[1]);
+                                    add2(sum[2], sum[3], f[2], f[3]);
+                                    if constexpr (C::kQ8) {
+                                        const float4 sc = *reinterpret_cast<const float4*>(vs + 32 * (k + h) + j);
+                                        f[0] *= sc.x; f[1] *= sc.y; f[2] *= sc.z; f[3] *= sc.w;
+                                    }
+                                    y[j / 2] = pack_bf16x2(f[0], f[1]);
+                                    y[j / 2 + 1] = pack_bf16x2(f[2], f[3]);
+                                }
+                                tc_st(t_s + 16 * (k + h), y);
+                            }
+                        }
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tc_wait_st();
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tc_wait_st();
+                    tc_fence_before();
+                    warp_arrive(p_full + st);
+                    if (C::kQ8 && i + kEvery < n) scales(tok0 + kEvery * kT);
+                    ++o_cnt;
+                    ++done;
                 }
-                tc_fence_before();
-                warp_arrive(p_full + st);
-                if (C::kQ8 && i + kEvery < n) scales(tok0 + kEvery * kT);
-                ++o_cnt;
-                ++done;
+                if (ok && i < n && warp_live) {  // O starts again
+                    ok = all_wait(o_done + st, (o_cnt - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    add_sums(m, done > kSpan, false);
+                }
             }
             if (!ok) break;
             uses += 2 * n;
@@ -464,6 +501,10 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
             if (done > 0) {
                 ok = all_wait(o_done + st, (o_cnt - 1) & 1);
                 if (!ok) break;
+                if (done > kSpan && warp_live) {
+                    tc_fence_after();
+                    add_sums(m, true, true);
+                }
             }
             ml[st * kT + r] = m;
             ml[(2 + st) * kT + r] = l;
@@ -618,6 +659,12 @@ TreePlan plan_tree_tc(int rows, int d) {
     // rows, 4 x 32K, they took 136 us against 117.
     const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kT ? kT : 2 * kT;
     return TreePlan{tile, kT, 148};
+}
+
+size_t tree_tc_sums(const TreePlan& plan, int grid, long long tiles, int d) {
+    // tiles of a stream; ds_tree_few.cu has them in tensor memory
+    const long long n = plan.tile_rows == 2 * kT ? tiles : (tiles + 1) / 2;
+    return plan.tile_rows < kT || n <= kSpan ? 0 : (size_t)grid * 2 * kT * d * sizeof(float);
 }
 
 cudaError_t launch_tree_few(const TreeParams& p, const TreeMaps& m, int type, int d, cudaStream_t st);

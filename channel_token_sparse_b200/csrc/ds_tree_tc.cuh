@@ -13,6 +13,13 @@ namespace {
 
 constexpr int kT = 128;  // tokens of a tile, and rows of a row block
 
+// The tensor cores cut off, rather than round, what a product adds to an
+// accumulator, so a long sum falls behind: by 1.2e-4 of itself after 256 tiles of
+// values of one sign, 1.9 % after 32K of them (4M tokens). So after kSpan tiles of
+// a stream its O goes into a second accumulator by rounded additions and starts
+// again: 6e-5 at most. Pieces of so many tiles are long ones; short ones do not pay.
+constexpr int kSpan = kTreeSpan;
+
 // ------------------------------------------------------------------ tcgen05
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }

@@ -429,7 +429,9 @@ DS_API ds_status ds_read_kv_paged(const void* k_pool, const void* v_pool, const 
  *              run at the same time need their own.
  * Scores, softmax statistics and sums are fp32. With bf16 and 8-bit caches the
  * products run on the tensor cores, and a weight exp(.) (times its row's
- * v_scale) is rounded to bf16 before its product with v. mask, seq_lens,
+ * v_scale) is rounded to bf16 before its product with v. The tensor cores cut
+ * off what they add to a sum: an output is up to 1e-4 of sum(weight * |v|) low,
+ * whatever the length. mask, seq_lens,
  * node_lens and the scales need 4-byte alignment, the other pointers 16. */
 DS_API ds_status ds_tree_decode_workspace_size(int b, int t, int hq, int hkv, int s, int d,
                                                ds_dtype kvdt, size_t* bytes);

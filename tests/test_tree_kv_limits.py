@@ -58,3 +58,20 @@ def test_write(lib, size, pool):
 def test_tree(lib, call, size):
     assert "s_cap" in TREE
     assert call(lib, **size, ws=FAKE, ws_bytes=1 << 50) == ds.DS_ERR_UNSUPPORTED, ds.last_error()
+
+
+@pytest.mark.parametrize("t,g,d,tiles,per_cta", [
+    (1, 8, 128, 8192, 0),       # up to 32 query rows: in tensor memory
+    (8, 8, 128, 256, 0),        # up to 128: two streams of 128 tiles
+    (8, 8, 128, 257, 2 * 128 * 128 * 4),
+    (16, 8, 64, 257, 2 * 128 * 64 * 4),
+    (17, 8, 128, 128, 0),       # more: each stream has every tile
+    (17, 8, 128, 129, 2 * 128 * 128 * 4),
+])
+def test_workspace_of_long_pieces(lib, t, g, d, tiles, per_cta):
+    """Second accumulators where a CTA's piece of an item may be longer than a
+    span of 128 tiles a stream: 148 items, then one item shared by all CTAs."""
+    rows = min(-(-t * g // 4) * 4, 256)
+    parts = 148 * 2 * rows * (d + 2) * 4
+    assert ds.tree_decode_workspace(148, t, g, 1, tiles * 128 - t, d) == parts + 148 * per_cta
+    assert ds.tree_decode_workspace(1, t, g, 1, tiles * 128 - t, d) <= parts

@@ -294,3 +294,78 @@ def test_pieces_of_more_than_a_second():
     ds.check_device()  # no wait gave up
     assert start.elapsed_time(end) > 1500.0
     assert bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", list(ROWS))
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_sums(kind, rows, d):
+    """A million tokens an entry of values of one sign, all with the weight 1
+    (the queries are 0), summed up by few CTAs: the output is the values' mean.
+    The weights, their sums and (8-bit: scales that are powers of 2) the products
+    are exact; what is off is the accumulation. A product adds 16 rows, in four
+    steps at most, each cutting off less than 2^-23 of the sum so far: 2^-21 of
+    it, half of that on average over a span of 128 tiles of 8 products. The spans
+    themselves are added in fp32."""
+    t, g = ROWS[rows]
+    page, blocks = 1 << 15, 32
+    b = 160 if t * g <= 256 else 40
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    k = torch.randn((1, 1, page, d), generator=gen, device="cuda")
+    v = 2.0 + torch.randn((1, 1, page, d), generator=gen, device="cuda")
+    ks = vs = None
+    if kind == "e4m3":
+        k, v = k.to(th.E4M3), (v * 16).to(th.E4M3)
+        ks, vs = torch.ones((1, 1, page), device="cuda"), torch.full((1, 1, page), 0.0625, device="cuda")
+        values = v.double() / 16
+    else:
+        k, v = k.bfloat16(), v.bfloat16()
+        values = v.double()
+    q = torch.zeros((b, t, g, d), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((b, blocks), dtype=torch.int32, device="cuda")
+    mask = torch.full((b, t, (t + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    out = ds.tree_decode_paged(q, k, v, table, blocks * page - t, mask=mask, k_scale=ks, v_scale=vs)
+    ds.check_device()
+    mean, size = values[0, 0].mean(0), values[0, 0].abs().mean(0)
+    tiles = blocks * page // 128
+    tol = (128 * 8 / 2 * 2.0 ** -21 + (tiles / 128 + 16) * 2.0 ** -24) * size
+    assert bool(((out.double() - mean).abs() <= tol).all()), float(((out.double() - mean).abs() / tol).max())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", list(ROWS))
+def test_maxima_that_move_late(kind, rows):
+    """Two kinds of pages, the second with keys 2.5 times as large, met after
+    thousands of tiles: what has been summed up by then, in both accumulators, is
+    scaled down. The scores, weights and sums are off as in treehelp.attention
+    (sums take a rounding a tile), the accumulation as in test_long_sums."""
+    t, g = ROWS[rows]
+    d, page, b = 128, 1 << 14, 80 if t * g <= 256 else 40
+    order = torch.tensor([0] * 40 + [1] * 3 + [0] * 21)
+    gen = torch.Generator(device="cuda").manual_seed(73)
+    k = torch.randn((2, 1, page, d), generator=gen, device="cuda")
+    v = 2.0 + torch.randn((2, 1, page, d), generator=gen, device="cuda")
+    k[1] *= 2.5
+    v[1] -= 3.0
+    ks = vs = None
+    if kind == "e4m3":
+        (k, ks), (v, vs) = quantised(k), quantised(v)
+    else:
+        k, v = k.bfloat16(), v.bfloat16()
+    q = torch.randn((b, t, g, d), generator=gen, device="cuda").bfloat16()
+    mask = torch.full((b, t, (t + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    s = len(order) * page - t
+    out = ds.tree_decode_paged(q, k, v, order.to(torch.int32).repeat(b, 1).cuda(), s, mask=mask, k_scale=ks, v_scale=vs)
+    ds.check_device()
+    kk, vv = (c[:, 0].cuda() for c in (th.values(k, ks), th.values(v, vs)))
+    times = torch.stack([(order == i).sum() for i in (0, 1)]).double().cuda()
+    pick = q[:: b - 1, :: max(t - 1, 1), 1].double()  # the first and the last entry and node
+    score = torch.einsum("btd,pnd->btpn", pick, kk) / d ** 0.5
+    size = torch.einsum("btd,pnd->btpn", pick.abs(), kk.abs()) / d ** 0.5
+    p = torch.softmax((score + times.log()[:, None]).flatten(2), -1).view_as(score)
+    want = torch.einsum("btpn,pnd->btd", p, vv)
+    sums = (s / 128 + 64) * th.F32
+    rel = 2 * (d + 4) * th.F32 * size + sums
+    bound = torch.einsum("btpn,pnd->btd", p * (rel + 2.0 ** -8 + 128 * 8 / 2 * 2.0 ** -21), vv.abs())
+    bound += (p * rel).sum((2, 3))[..., None] * want.abs()
+    th.check(out[:: b - 1, :: max(t - 1, 1), 1], want.cpu(), bound.cpu())
