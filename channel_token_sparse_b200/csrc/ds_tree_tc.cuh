@@ -421,17 +421,27 @@ __device__ __forceinline__ void copy_queries(const TreeParams& p, uint8_t* q, ui
         if (rows <= 0) continue;
         if (!__all_sync(0xffffffffu, wait(q_empty, ph, kPieceWait))) return;
         ph ^= 1;
-#pragma unroll 8
+        // All of a thread's reads are in flight together: through registers, eight at a
+        // time, a piece of 256 rows began with eight waits (64 nodes x 4 heads over 128K
+        // 209 us instead of 176, 16 nodes over 4 x 32K 114 instead of 107).
+#pragma unroll 4
         for (int x = tid; x < QR * kChunks; x += 64) {
             const int row = x / kChunks, c = x % kChunks;
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (row < rows)
-                y = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                         q_offset(p, w.e, w.h, row0 + row, D) + c * 8));
-            if constexpr (Q8)
-                y = make_uint4(__byte_perm(y.x, y.y, 0x5410), __byte_perm(y.x, y.y, 0x7632),
-                               __byte_perm(y.z, y.w, 0x5410), __byte_perm(y.z, y.w, 0x7632));
-            *reinterpret_cast<uint4*>(q + (row / kB) * kB * D * 2 + tile_at(row % kB, c, kB)) = y;
+            const size_t at = row < rows ? q_offset(p, w.e, w.h, row0 + row, D) : 0;
+            cp_async16_zfill(q + (row / kB) * kB * D * 2 + tile_at(row % kB, c, kB), static_cast<const uint16_t*>(p.q) + at + c * 8,
+                             row < rows);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        if constexpr (Q8) {
+#pragma unroll 4
+            for (int x = tid; x < QR * kChunks; x += 64) {  // (this thread's own)
+                const int row = x / kChunks, c = x % kChunks;
+                uint4* at = reinterpret_cast<uint4*>(q + (row / kB) * kB * D * 2 + tile_at(row % kB, c, kB));
+                const uint4 y = *at;
+                *at = make_uint4(__byte_perm(y.x, y.y, 0x5410), __byte_perm(y.x, y.y, 0x7632),
+                                 __byte_perm(y.z, y.w, 0x5410), __byte_perm(y.z, y.w, 0x7632));
+            }
         }
         proxy_fence();
         warp_arrive(q_full);
