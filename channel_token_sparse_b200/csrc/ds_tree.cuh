@@ -211,8 +211,8 @@ enum TreeType { kTreeF32 = 0, kTreeBF16 = 1, kTreeE4M3 = 2 };
 struct TreePlan { int tile_rows, tile_tokens, grid; };
 TreePlan plan_tree_simt(int rows, int d);
 cudaError_t launch_tree_simt(const TreeParams& p, int d, cudaStream_t st);
-// bf16 and e4m3 (ds_tree_tc.cu; up to 32 query rows: ds_tree_few.cu).
-TreePlan plan_tree_tc(int rows, int d);
+// bf16 and e4m3 (ds_tree_tc.cu; up to 16 query rows, e4m3 32: ds_tree_few.cu).
+TreePlan plan_tree_tc(int rows, int type);
 // Bytes of their second accumulators, for pieces of at most `tiles` token tiles.
 size_t tree_tc_sums(const TreePlan& plan, int grid, long long tiles, int d);
 cudaError_t launch_tree_tc(const TreeParams& p, int type, int d, cudaStream_t st);

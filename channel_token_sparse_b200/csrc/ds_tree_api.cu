@@ -155,7 +155,7 @@ ds_status tree_shape(int b, int t, int hq, int hkv, int s, int d, ds_dtype kvdt,
         DS_FAIL(DS_ERR_UNSUPPORTED, "k/v dtype %d (supported: f32, bf16, e4m3)", (int)kvdt);
     o->type = kvdt == DS_F32 ? ds::kTreeF32 : kvdt == DS_BF16 ? ds::kTreeBF16 : ds::kTreeE4M3;
     const int rows = t * (hq / hkv);
-    o->plan = o->type == ds::kTreeF32 ? ds::plan_tree_simt(rows, d) : ds::plan_tree_tc(rows, d);
+    o->plan = o->type == ds::kTreeF32 ? ds::plan_tree_simt(rows, d) : ds::plan_tree_tc(rows, o->type);
     o->n_mt = (rows + o->plan.tile_rows - 1) / o->plan.tile_rows;
     // a multiple of 4 keeps every place, and the values behind its rows' statistics, 16-byte aligned
     o->part_rows = ((rows < o->plan.tile_rows ? rows : o->plan.tile_rows) + 3) / 4 * 4;

@@ -1,5 +1,5 @@
-// ds_tree_few.cu -- tree attention of up to 32 query rows a kv head over bf16
-// and 8-bit caches, on the tensor cores, for sm_100a.
+// ds_tree_few.cu -- tree attention of up to 16 (8-bit caches: 32) query rows a kv
+// head over bf16 and 8-bit caches, on the tensor cores, for sm_100a.
 //
 // The products are taken the other way round from ds_tree_tc.cu: S^T = K Q^T
 // and O^T += V^T P^T, so that the 128 rows the tensor cores want are the
@@ -15,10 +15,11 @@
 // only when one of its scores passes it by 8 (see ds_tree_tc.cu); whether one
 // does is the only thing the four warps agree on in every tile. Sums stay a
 // thread's own until the end. Measured on a B200: one token of 32 heads over
-// 256K 8-bit tokens 521 us (65 % of the copy rate; widening the codes and the
-// issue of the products bound it), 8 nodes over 8 x 4K 8-bit 100 us, 7 nodes x
-// 4 heads over 16 x up to 8K bf16 in pages 80 us of a 93 us step. Roles, ring, loaders and the treatment of values
-// that are not finite in tree rows are those of ds_tree_tc.cu.
+// 256K 8-bit tokens 502 us (67 % of the copy rate; widening the codes and the
+// issue of the products bound it), 8 nodes over 8 x 4K 8-bit 97 us, one token of 8
+// heads of 4 over 4 x 128K bf16 329 us (all of the copy rate). Roles, ring, loaders
+// and the treatment of values that are not finite in tree rows are those of
+// ds_tree_tc.cu.
 #include "ds_tree_tc.cuh"
 
 namespace ds {
@@ -549,11 +550,9 @@ cudaError_t run(const TreeParams& p, const TreeMaps& m, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_tree_few(const TreeParams& p, const TreeMaps& m, int type, int d, cudaStream_t st) {
-#define DS_N(TY, D_) \
-    (p.tile_rows == 16 ? run<TY, D_, 16>(p, m, st) : run<TY, D_, 32>(p, m, st))
-    if (type == kTreeBF16) return d == 64 ? DS_N(kTreeBF16, 64) : DS_N(kTreeBF16, 128);
-    return d == 64 ? DS_N(kTreeE4M3, 64) : DS_N(kTreeE4M3, 128);
-#undef DS_N
+    if (type == kTreeBF16) return d == 64 ? run<kTreeBF16, 64, 16>(p, m, st) : run<kTreeBF16, 128, 16>(p, m, st);
+    if (p.tile_rows == 16) return d == 64 ? run<kTreeE4M3, 64, 16>(p, m, st) : run<kTreeE4M3, 128, 16>(p, m, st);
+    return d == 64 ? run<kTreeE4M3, 64, 32>(p, m, st) : run<kTreeE4M3, 128, 32>(p, m, st);
 }
 
 }  // namespace ds

@@ -652,12 +652,17 @@ cudaError_t make_tree_maps(const TreeParams& p, int type, int d, TreeMaps* m) {
     return cudaSuccess;
 }
 
-TreePlan plan_tree_tc(int rows, int d) {
-    (void)d;
-    // Up to 32 query rows the products with tokens as rows (ds_tree_few.cu) are
-    // faster: 28 rows, 16 x 8K bf16 in pages, step of 92 us against 98; with 64
-    // rows, 4 x 32K, they took 136 us against 117.
-    const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kT ? kT : 2 * kT;
+TreePlan plan_tree_tc(int rows, int type) {
+    // us a call, 4 x 32K tokens of 8 kv heads unless stated. Products with tokens as
+    // rows (ds_tree_few.cu) or with queries as rows:
+    //   16 rows bf16 100 or 105 (512 tokens 14.8 or 16.6), 8-bit 87 or 130;
+    //   20 rows bf16 110 or 105, 8-bit 108 or 130; 32 rows bf16 112 or 106, 8-bit
+    //   109 or 130; 28 rows, 16 x 8K bf16 in pages, with the write 91 or 82.
+    // One block of 128 rows or two, that share the tiles they read:
+    //   128 rows bf16 114 or 146, 8-bit 139 or 192 (two, half of them empty);
+    //   132 rows bf16 189 or 160, 8-bit 235 or 209.
+    const int few = type == kTreeE4M3 ? 32 : 16;
+    const int tile = rows <= 16 ? 16 : rows <= few ? few : rows <= kT ? kT : 2 * kT;
     return TreePlan{tile, kT, 148};
 }
 
