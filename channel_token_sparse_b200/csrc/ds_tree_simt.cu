@@ -5,10 +5,9 @@
 // exponents) of 8 to 32 query rows, their new maxima, weights 2^(s - m), and the
 // weighted values, all in fp32. A tile's K and V rows are read into
 // shared memory once and serve the row tile. Kept simple: fp32 caches are the
-// small and the reference ones (4 nodes over 512 tokens: 12.5 us, two launches'
+// small and the reference ones (4 nodes over 512 tokens: 11.4 us, two launches'
 // latency; 8 nodes x 4 heads over 4 x 4K 166 us against 21 us of bytes: the tile of
-// keys is read from shared memory once a row; one node x 8 heads over 2 x 16K 114 us
-// with row tiles of 8, 305 us with 32).
+// keys is read from shared memory once a row).
 #include <math.h>
 
 #include "ds_tree.cuh"
@@ -18,8 +17,8 @@ namespace ds {
 namespace {
 
 constexpr int kNT = 256;
-// Query rows of a row tile: 32, or few where there are no more (a tile costs its
-// rows' arithmetic whether they exist or not; four channels a thread at least).
+// Query rows of a row tile: 32, or few (a tile costs its rows' arithmetic whether
+// they exist or not; four channels a thread at least): see plan_tree_simt.
 constexpr int kMany = 32;
 template <int D> constexpr int kFew = D == 128 ? 8 : 16;
 constexpr int kT = 64;     // tokens of a token tile
@@ -47,7 +46,7 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const __grid_constant
     TreePiece w;
     constexpr int kC = kNT / kR;        // threads of a row
     constexpr int kO = D / kC;          // output channels of a thread
-    const int orow = tid / kC, oc = (tid % kC) * 4;  // its row; channels oc + 32 j ..
+    const int orow = tid / kC, oc = (tid % kC) * 4;  // its row; channels oc + 4 kC j ..
     while (next_piece(p, cur, u, end, w)) {
         const int row0 = w.mt * p.tile_rows;
         const int rows = min(kR, w.nodes * p.G - row0);
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(kNT) ds_tree_simt_kernel(const __grid_constant
                 *reinterpret_cast<float4*>(sv + t * D + c) = fv[j];
             }
             __syncthreads();
-            // scores: a thread takes one row and tokens t = tid % 8 + 8 j
+            // scores: a thread takes one row and tokens t = tid % kC + kC j
             {
                 const int r = tid / kC;
                 float acc[kT / kC] = {};
@@ -194,8 +193,15 @@ cudaError_t run(const TreeParams& p, cudaStream_t st) {
 }  // namespace
 
 TreePlan plan_tree_simt(int rows, int d) {
+    // A tile of few rows takes a third (64 channels: five ninths) of the time of one of
+    // 32. One or more of them against the others, us a call of 8 kv heads over 2 x 16K:
+    //   128 channels  8 rows 108 or 297; 9 to 16 201 or 297; 17 to 24 295 or 299;
+    //                 25 to 32 385 or 299; 33 to 40 483 or 585; 41 to 48 578 or 585; 64 756 or 585
+    //   64 channels   16 rows 93 or 162; 17 to 32 178 or 162; 33 to 48 258 or 312; 64 344 or 312
     const int few = d == 64 ? kFew<64> : kFew<128>;
-    return TreePlan{rows <= few ? few : kMany, kT, 2 * 148};
+    const int n_few = (rows + few - 1) / few, n_many = (rows + kMany - 1) / kMany;
+    const bool cheaper = d == 64 ? 5 * n_few <= 9 * n_many : n_few <= 3 * n_many;
+    return TreePlan{cheaper ? few : kMany, kT, 2 * 148};
 }
 
 cudaError_t launch_tree_simt(const TreeParams& p, int d, cudaStream_t st) {

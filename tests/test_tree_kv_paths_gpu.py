@@ -9,6 +9,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import channel_token_sparse_b200 as ds  # noqa: E402
+import test_tree_kv_gpu as sized  # noqa: E402
 from test_tree_kv_gpu import caches, chain, cu, paged, quantised, randn  # noqa: E402
 
 
@@ -369,3 +370,18 @@ def test_maxima_that_move_late(kind, rows):
     bound = torch.einsum("btpn,pnd->btd", p * (rel + 2.0 ** -8 + 128 * 8 / 2 * 2.0 ** -21), vv.abs())
     bound += (p * rel).sum((2, 3))[..., None] * want.abs()
     th.check(out[:: b - 1, :: max(t - 1, 1), 1], want.cpu(), bound.cpu())
+
+
+@pytest.mark.parametrize("case", [
+    # either side of the row counts at which another kernel or row tile takes over
+    ("f32", 2, 12, 2, 2, 128, 300, [300, 9], 0, "tree"), ("f32", 1, 25, 2, 2, 128, 300, None, 16, "tree"),
+    ("f32", 2, 41, 2, 2, 128, 130, [0, 130], 0, "tree"), ("f32", 1, 49, 2, 2, 128, 200, None, 0, "tree"),
+    ("f32", 2, 20, 4, 2, 64, 300, [300, 64], 0, "tree"), ("f32", 1, 49, 2, 2, 64, 300, None, 1, "tree"),
+    ("bf16", 2, 16, 2, 2, 128, 400, [400, 200], 0, "tree"), ("bf16", 2, 17, 2, 2, 128, 400, [400, 200], 16, "tree"),
+    ("bf16", 1, 32, 2, 2, 64, 400, None, 0, "tree"), ("bf16", 1, 128, 1, 1, 64, 300, None, 0, "tree"),
+    ("bf16", 1, 129, 1, 1, 64, 300, None, 0, "tree"), ("e4m3", 1, 32, 2, 2, 64, 400, None, 0, "tree"),
+    ("e4m3", 1, 33, 2, 2, 128, 400, None, 16, "tree"), ("e4m3", 1, 128, 1, 1, 64, 300, None, 0, "tree"),
+    ("e4m3", 1, 129, 1, 1, 64, 300, None, 0, "tree"),
+])
+def test_borders_between_kernels(case):
+    sized.test_tree_decode(*case)
