@@ -575,12 +575,15 @@ class _Prepared:
     (an event), and streams that run side by side have a handle each. A graph
     that captured a call needs the handle for as long as it is replayed."""
 
-    def _bind(self, fn, args, dev, stream, keep, result):
+    def _bind(self, fn, args, dev, stream, keep, result, once=False):
         self._fn, self._args, self._dev, self._stream = fn, args, dev, stream
         self._keep = keep  # keeps the memory alive
         self._result = result
         # streams that the tensors' memory waits for when it is freed: the one it belongs to
-        self._streams = {_torch().cuda.current_stream(dev).cuda_stream} if stream is None else set()
+        # (a handle that is called right away and dropped does not look it up: the call does)
+        self._streams = set()
+        if stream is None:
+            self._streams = None if once else {_torch().cuda.current_stream(dev).cuda_stream}
 
     def _record(self, stream):
         """The allocator hears of a stream that the tensors were not made on."""
@@ -597,7 +600,9 @@ class _Prepared:
         dev = self._dev
         stream = torch.cuda.current_stream(dev) if self._stream is None else self._stream
         s = stream.cuda_stream
-        if s not in self._streams:
+        if self._streams is None:
+            self._streams = {s}
+        elif s not in self._streams:
             self._record(stream)
         if torch.cuda.current_device() != dev.index:
             with torch.cuda.device(dev):
@@ -644,7 +649,7 @@ class PreparedWriteKV(_Prepared):
 
     def __init__(self, q, k, v, k_cache, v_cache, starts=None, positions=None, lens=None, q_weight=None,
                  k_weight=None, eps: float = 1e-6, inv_freq=None, rope: int = DS_ROPE_HALF, k_scale=None,
-                 v_scale=None, block_table=None, q_out=None, stream=None):
+                 v_scale=None, block_table=None, q_out=None, stream=None, _once=False):
         torch = _torch()
         dev = _on_one_device(k, v, q, k_cache, v_cache, starts, positions, lens, q_weight, k_weight, inv_freq,
                              k_scale, v_scale, block_table, q_out)
@@ -706,7 +711,7 @@ class PreparedWriteKV(_Prepared):
             args = args + tail + [ptr(block_table), block_table.shape[1], k_cache.shape[2], k_cache.shape[0]]
         self.q_out = q_out
         self._bind(fn, args, dev, stream, (q, k, v, k_cache, v_cache, starts, positions, lens, q_weight, k_weight,
-                                           inv_freq, k_scale, v_scale, block_table), q_out)
+                                           inv_freq, k_scale, v_scale, block_table), q_out, _once)
 
 
 def write_kv(q, k, v, k_cache, v_cache, **kw):
@@ -717,7 +722,7 @@ def write_kv(q, k, v, k_cache, v_cache, **kw):
     (or None) gets its norm and rotation into q_out, which is returned. q, k
     and v may be views of one fused projection. Caches [B, Hkv, S_cap, D], or
     pools with block_table. Arguments as PreparedWriteKV's; see ds_write_kv."""
-    return PreparedWriteKV(q, k, v, k_cache, v_cache, **kw)()
+    return PreparedWriteKV(q, k, v, k_cache, v_cache, _once=True, **kw)()
 
 
 def read_kv(k, v, k_scale, v_scale, s: int, seq_lens=None, block_table=None, dtype=None, k_out=None, v_out=None,
@@ -764,7 +769,7 @@ def read_kv(k, v, k_scale, v_scale, s: int, seq_lens=None, block_table=None, dty
         fn = lib().ds_read_kv_paged
         args = [ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), ptr(block_table), block_table.shape[1], k.shape[2],
                 k.shape[0], ptr(seq_lens), b, hkv, int(s), d, *tail]
-    call._bind(fn, args, dev, stream, (k, v, k_scale, v_scale, seq_lens, block_table), (k_out, v_out))
+    call._bind(fn, args, dev, stream, (k, v, k_scale, v_scale, seq_lens, block_table), (k_out, v_out), True)
     return call()
 
 
@@ -806,7 +811,7 @@ class PreparedTreeDecode(_Prepared):
     _S_ARG = {False: 13, True: 17}
 
     def __init__(self, q, k, v, s: int, mask=None, seq_lens=None, node_lens=None, k_scale=None, v_scale=None,
-                 block_table=None, out=None, out_dtype=None, sm_scale: float = 0.0, ws=None, stream=None):
+                 block_table=None, out=None, out_dtype=None, sm_scale: float = 0.0, ws=None, stream=None, _once=False):
         torch = _torch()
         dev = _on_one_device(q, k, v, mask, seq_lens, node_lens, k_scale, v_scale, block_table, out, ws)
         for t in (q, k, v, mask, seq_lens, node_lens, k_scale, v_scale, block_table, out, ws):
@@ -850,7 +855,7 @@ class PreparedTreeDecode(_Prepared):
             args = head + [ptr(block_table), block_table.shape[1], k.shape[2], k.shape[0], ptr(seq_lens),
                            ptr(node_lens), b, t, hq, hkv, int(s)] + tail
         self.out, self._s_at, self._s_max = out, self._S_ARG[block_table is not None], int(s)
-        self._bind(fn, args, dev, stream, (q, k, v, mask, seq_lens, node_lens, k_scale, v_scale, block_table, ws), out)
+        self._bind(fn, args, dev, stream, (q, k, v, mask, seq_lens, node_lens, k_scale, v_scale, block_table, ws), out, _once)
 
     def set_length(self, s: int) -> None:
         if not 0 <= s <= self._s_max:
@@ -865,10 +870,10 @@ def tree_decode(q, k, v, s: int, **kw):
     mask as tree_mask makes it (None: a chain). float8_e4m3fn caches need
     k_scale and v_scale. Returns out [B, T, Hq, D]. Arguments as
     PreparedTreeDecode's; see ds_tree_decode."""
-    return PreparedTreeDecode(q, k, v, s, **kw)()
+    return PreparedTreeDecode(q, k, v, s, _once=True, **kw)()
 
 
 def tree_decode_paged(q, k_pool, v_pool, block_table, s: int, **kw):
     """tree_decode over pools [num_blocks, Hkv, page, D] with block_table
     [B, max_blocks]."""
-    return PreparedTreeDecode(q, k_pool, v_pool, s, block_table=block_table, **kw)()
+    return PreparedTreeDecode(q, k_pool, v_pool, s, block_table=block_table, _once=True, **kw)()

@@ -86,3 +86,11 @@ def test_captured_calls_record_at_the_first_real_one(cuda):
     cuda.current = Stream(8)
     h()
     assert [t.recorded for t in tensors] == [[8]] * 3
+
+
+def test_a_call_made_at_once_takes_the_stream_of_its_call(cuda):
+    kept, out = Tensor(), Tensor()
+    for stream, recorded in ((None, []), (Stream(12), [12])):
+        h = ds._Prepared()
+        h._bind(lambda *a: ds.DS_OK, [], DEV, stream, (kept,), out, True)
+        assert h() is out and kept.recorded == recorded and out.recorded == recorded
