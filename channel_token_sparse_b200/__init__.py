@@ -777,7 +777,8 @@ def tree_mask(parents):
     """The mask of drafted trees from their parents [B, T] (int tensor: the
     index of each node's parent, which is a smaller one, or -1 for the prefix):
     node i sees itself and its ancestors. int32 [B, T, ceil(T / 32)] on
-    parents' device; computed with torch, outside the decode path."""
+    parents' device. Worked out on the host, a node at a time: reads parents
+    back where they are on the GPU, and cannot be captured in a graph."""
     torch = _torch()
     b, t = parents.shape
     p = parents.to("cpu", torch.int64)
@@ -868,7 +869,8 @@ def tree_decode(q, k, v, s: int, **kw):
     [B, Hkv, S_cap, D] that hold a prefix of s tokens (seq_lens[b], at most s)
     and, in the T rows behind it, the drafted tokens' own keys and values;
     mask as tree_mask makes it (None: a chain). float8_e4m3fn caches need
-    k_scale and v_scale. Returns out [B, T, Hq, D]. Arguments as
+    k_scale and v_scale; a row that holds a NaN code needs the scale NaN, as
+    write_kv leaves it (a conversion of out-of-range values by torch does not). Returns out [B, T, Hq, D]. Arguments as
     PreparedTreeDecode's; see ds_tree_decode."""
     return PreparedTreeDecode(q, k, v, s, _once=True, **kw)()
 

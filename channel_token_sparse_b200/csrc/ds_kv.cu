@@ -13,8 +13,9 @@
 // sine and cosine each) are computed once and serve all of its heads.
 //
 // Measured on a B200: 8192 tokens of 32 + 8 + 8 heads of 128 in bf16, 201 MB,
-// 48 us (65 % of the copy rate: the chain from a head's load to its store);
-// the same into 8-bit pages 52 us (issue); 32 single tokens 6 us in the kernel.
+// 47.5 us (65 % of the copy rate: the chain from a head's load to its store), in
+// fp32 70 us (87 %); into 8-bit pages 51 us (the same chain, and issue); 32 single
+// tokens 6 us in the kernel.
 //
 // Read: 16 codes a thread and step, times the row's scale. 65536 rows of 8
 // heads, 407 MB: 71 us, 87 % of the copy rate.

@@ -19,11 +19,14 @@
 // the queries. 8-bit tiles land in slots of their own and warps 12 to 19 widen
 // them to bf16 (exact) into the ring; their rows' scales multiply S and P.
 //
-// Measured on a B200: 16 nodes x 4 heads over 4 x 32K bf16 119 us (69 % of the
-// copy rate; MT = 1), 64 nodes x 4 heads over 128K bf16 220 us (625 TFLOP/s;
-// MT = 2). What bounds MT = 2 is the chain of a stream's tile: softmax (1.7K
-// cycles), PV, S and the wake-ups between them, 3.9K cycles against the 2K that
-// the products of both streams take.
+// Measured on a B200: 16 nodes x 4 heads over 4 x 32K bf16 107 us (77 % of the
+// copy rate; MT = 1; 8-bit 132), 64 nodes x 4 heads over 128K bf16 176 us (780
+// TFLOP/s; MT = 2; 8-bit 252). What bounds MT = 2 is the chain of a stream's tile:
+// softmax, PV, S and the wake-ups between them (tensor pipe and special-function
+// unit both half busy).
+//
+// P is rounded to bf16 (2^-9 of a weight at most, each its own way), which is what
+// the products take; a second product for the remainders would double P V.
 //
 // The products take every row of V with every weight, and 0 * NaN is NaN, so
 // the softmax warps tidy a tile that reaches past the prefix: rows past the
@@ -81,7 +84,7 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
     const __grid_constant__ TreeParams p, const __grid_constant__ TreeMaps maps) {
     using C = Cfg<TYPE, D, MT>;
     constexpr int NS = C::kStages;
-        extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     float* ml = reinterpret_cast<float*>(smem + C::oMl);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::oBar);
     uint64_t* empty = full + NS;
@@ -386,8 +389,9 @@ __global__ void __launch_bounds__(Cfg<TYPE, D, MT>::kThreads, 1) ds_tree_tc_kern
                             }
                         }
                         // The tile's maximum. MT = 2, where the softmax is on the critical path:
-                        // the scores stay in registers from here on (64 nodes over 128K: 217 ->
-                        // 210 us; one row block is 6 % slower so); else they are read once more.
+                        // the scores stay in registers from here on (64 nodes over 128K 177 us
+                        // or 185, for all that 250 bytes a thread are spilled; one row block of
+                        // 64 rows 117 us so, or 108); else they are read once more.
                         constexpr int kHeld = C::kQ8 || MT == 1 ? 2 : 4;
                         uint32_t x[kHeld][32];
                         float mx = -INFINITY;

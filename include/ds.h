@@ -354,7 +354,7 @@ typedef enum {
  *               or NULL (t)
  *   q_out       [b, t, hq, d] dtype dt; may be q itself where q has that layout
  *   k_cache, v_cache  dtype cache_dt: dt, or DS_E4M3 with k_scale and v_scale
- * Two tokens of one call that go to the same row leave either's contents.
+ * Two tokens of one call that go to the same row leave a mixture of both there.
  * inv_freq, positions, starts, lens and the scales need 4-byte alignment, the
  * other pointers 16. DS_ERR_UNSUPPORTED for b * t > 2^30, more than 2^20 heads of
  * a kind, a cache of 2^40 elements or more, or a cache dtype that is neither. */
