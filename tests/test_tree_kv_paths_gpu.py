@@ -385,3 +385,40 @@ def test_maxima_that_move_late(kind, rows):
 ])
 def test_borders_between_kernels(case):
     sized.test_tree_decode(*case)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", list(ROWS))
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_pieces_repeat(kind, rows, d):
+    """Pieces of several spans with maxima that move: the same bits every time,
+    whatever the workspace holds before, and captured."""
+    t, g = ROWS[rows]
+    page, blocks, b = 1 << 13, 32, 150 if t * g <= 256 else 40
+    gen = torch.Generator(device="cuda").manual_seed(79)
+    k, v = (torch.randn((blocks, 1, page, d), generator=gen, device="cuda") for _ in "kv")
+    k *= torch.linspace(0.5, 2.0, blocks, device="cuda")[:, None, None, None]
+    ks = vs = None
+    if kind == "e4m3":
+        (k, ks), (v, vs) = quantised(k), quantised(v)
+    else:
+        k, v = k.bfloat16(), v.bfloat16()
+    q = torch.randn((b, t, g, d), generator=gen, device="cuda").bfloat16()
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda").repeat(b, 1)
+    s = blocks * page - t
+    ws = torch.empty(ds.tree_decode_workspace(b, t, g, 1, s, d, ds.DS_E4M3 if kind == "e4m3" else ds.DS_BF16),
+                     dtype=torch.uint8, device="cuda")
+    call = ds.PreparedTreeDecode(q, k, v, s, k_scale=ks, v_scale=vs, block_table=table, ws=ws)
+    first = call().clone()
+    assert bool(torch.isfinite(first).all())
+    for fill in (0, 255, 127, 255):
+        ws.fill_(fill)
+        call.out.zero_()
+        assert torch.equal(call(), first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    call.out.zero_()
+    graph.replay()
+    assert torch.equal(call.out, first)
+    ds.check_device()
